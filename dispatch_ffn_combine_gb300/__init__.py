@@ -39,8 +39,12 @@ ENTRY_POINTS = (
     "mk_moe_grouped_gemm", "mk_moe_dispatch_gemm_workspace_size", "mk_moe_dispatch_gemm",
     "mk_moe_route_approx_logits", "mk_moe_workspace_region", "mk_moe_ep_regroup_workspace_size",
     "mk_moe_ep_regroup",
+    "mk_moe_grouped_dgrad", "mk_moe_grouped_wgrad", "mk_moe_ckpt8_save", "mk_moe_ckpt8_dispatch",
+    "mk_moe_swiglu_ckpt8", "mk_moe_swiglu_ckpt8_bwd", "mk_moe_layernorm", "mk_moe_layernorm_bwd_workspace_size",
+    "mk_moe_layernorm_bwd",
 )
-_SIZE_RESULT = ("mk_moe_workspace_size", "mk_moe_dispatch_gemm_workspace_size", "mk_moe_ep_regroup_workspace_size")
+_SIZE_RESULT = ("mk_moe_workspace_size", "mk_moe_dispatch_gemm_workspace_size", "mk_moe_ep_regroup_workspace_size",
+                "mk_moe_layernorm_bwd_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +105,17 @@ def load_library():
         lib.mk_moe_ep_regroup_workspace_size.restype = SZ
         lib.mk_moe_ep_regroup_workspace_size.argtypes = [I, I]
         lib.mk_moe_ep_regroup.argtypes = [P, P, P, I, I, I64, I, I, P, P, SZ, P]
+        F = ctypes.c_float
+        lib.mk_moe_grouped_dgrad.argtypes = [P, P, P, P, P, I64, I, I, I, P, P, SZ, P]
+        lib.mk_moe_grouped_wgrad.argtypes = [P, P, P, I64, I, I, I, P, I, I, P, SZ, P]
+        lib.mk_moe_ckpt8_save.argtypes = [P, I64, I, P, P, P]
+        lib.mk_moe_ckpt8_dispatch.argtypes = [P, P, P, I64, I, I, P, P, SZ, P]
+        lib.mk_moe_swiglu_ckpt8.argtypes = [P, P, I64, I, P, P, P, P]
+        lib.mk_moe_swiglu_ckpt8_bwd.argtypes = [P, P, P, P, I64, I, P, P, P, P, P]
+        lib.mk_moe_layernorm.argtypes = [P, I, P, P, I64, I, F, P, P, P, P]
+        lib.mk_moe_layernorm_bwd_workspace_size.restype = SZ
+        lib.mk_moe_layernorm_bwd_workspace_size.argtypes = [I64, I]
+        lib.mk_moe_layernorm_bwd.argtypes = [P, P, I, P, P, P, P, I64, I, P, P, P, P, SZ, P]
         for name in ENTRY_POINTS:
             if name not in _SIZE_RESULT + ("mk_moe_status_string",):
                 getattr(lib, name).restype = I
@@ -499,3 +514,229 @@ def mk_moe_ep_regroup(rows_in, counts, to_expert_major, rows_out=None, expert_of
                                           _stream(stream))
     _check(st, "mk_moe_ep_regroup")
     return rows_out
+
+
+# ----------------------------------------------------------------- training
+
+MK_TYPE_BF16 = 0
+MK_TYPE_FP32 = 1
+_TYPES = {torch.bfloat16: MK_TYPE_BF16, torch.float32: MK_TYPE_FP32}
+
+
+def _buffer(t, name, dtype, shape, like, stream):
+    """`t` checked as an output or workspace on `like`'s device, or a new tensor.
+
+    A new tensor belongs to the current stream's memory; where the call runs on
+    another one, the allocator is told, so that the memory is not handed out
+    again before that stream is done with it."""
+    if t is not None:
+        return _same_device(_need(t, dtype, shape, name), name, like)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _same_device(t, name, like):
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return t
+
+
+def _input(t, dtype, shape, name, like=None):
+    _need(t, dtype, shape, name)
+    return t if like is None else _same_device(t, name, like)
+
+
+def _two_dims(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _workspace(ws, nbytes, like, stream):
+    if ws is None:
+        return _buffer(None, "ws", torch.uint8, (nbytes,), like, stream)
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous() or not ws.is_cuda:
+        raise ValueError("ws must be a contiguous CUDA tensor of bytes")
+    return _same_device(ws, "ws", like)
+
+
+def _expert_weight(w, name, n, like):
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if w.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got {w.dim()}")
+    E, _, d = w.shape
+    _input(w, torch.bfloat16, (E, n, d), name, like)
+    return E, d
+
+
+def mk_moe_grouped_dgrad(dout, expert_offsets, w, dout2=None, w2=None, dx=None, ws=None, stream=None):
+    """Input gradient of the grouped GEMM: dx[r] = dout[r] @ w[e] (+ dout2[r] @ w2[e]) for the
+    rows r of expert e.  dout, dout2 [S, n] and w, w2 [E, n, d] bf16; returns dx [S, d] bf16."""
+    S, n = _two_dims(dout, "dout")
+    _input(dout, torch.bfloat16, (S, n), "dout")
+    E, d = _expert_weight(w, "w", n, dout)
+    _input(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dout)
+    if (dout2 is None) != (w2 is None):
+        raise ValueError("dout2 and w2 go together")
+    if dout2 is not None:
+        _input(dout2, torch.bfloat16, (S, n), "dout2", dout)
+        _input(w2, torch.bfloat16, (E, n, d), "w2", dout)
+    dx = _buffer(dx, "dx", torch.bfloat16, (S, d), dout, stream)
+    ws = _workspace(ws, 256 + 4 * (E + 1), dout, stream)
+    with torch.cuda.device(dout.device):
+        st = load_library().mk_moe_grouped_dgrad(_p(dout), _p(expert_offsets), _p(w), _p(dout2), _p(w2), S, d, E, n,
+                                                 _p(dx), _p(ws), ws.numel(), _stream(stream))
+    _check(st, "mk_moe_grouped_dgrad")
+    return dx
+
+
+def mk_moe_grouped_wgrad(dout, expert_offsets, x_perm, dw=None, accumulate=False, dtype=torch.float32, ws=None,
+                         stream=None):
+    """Weight gradient of the grouped GEMM: dw[e] (+)= dout[rows of e].T @ x_perm[rows of e].
+
+    dout [S, n] and x_perm [S, d] bf16; returns dw [E, n, d] in `dtype` (fp32 or bf16; the passed
+    dw's own type when there is one).  accumulate adds to the passed fp32 dw; otherwise dw is
+    overwritten (zeros for an expert without rows)."""
+    S, n = _two_dims(dout, "dout")
+    _input(dout, torch.bfloat16, (S, n), "dout")
+    d = _two_dims(x_perm, "x_perm")[1]
+    _input(x_perm, torch.bfloat16, (S, d), "x_perm", dout)
+    if not isinstance(expert_offsets, torch.Tensor) or expert_offsets.dim() != 1 or expert_offsets.numel() < 2:
+        raise ValueError("expert_offsets must be a 1-D tensor of E + 1 row offsets")
+    E = expert_offsets.numel() - 1
+    _input(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dout)
+    dtype = dw.dtype if isinstance(dw, torch.Tensor) else dtype
+    if dtype not in _TYPES:
+        raise TypeError(f"dw must be torch.float32 or torch.bfloat16, got {dtype}")
+    if accumulate and (dw is None or dtype != torch.float32):
+        raise ValueError("accumulate needs an fp32 dw to add to")
+    dw = _buffer(dw, "dw", dtype, (E, n, d), dout, stream)
+    ws = _workspace(ws, 256, dout, stream)
+    with torch.cuda.device(dout.device):
+        st = load_library().mk_moe_grouped_wgrad(_p(dout), _p(expert_offsets), _p(x_perm), S, d, E, n, _p(dw),
+                                                 _TYPES[dtype], 1 if accumulate else 0, _p(ws), ws.numel(),
+                                                 _stream(stream))
+    _check(st, "mk_moe_grouped_wgrad")
+    return dw
+
+
+def mk_moe_ckpt8_save(x, codes=None, scales=None, stream=None):
+    """Tokens x [T, d] bf16 kept in 8 bits: returns (codes [T, d] uint8, scales [T, d / 32] uint8)."""
+    T, d = _two_dims(x, "x")
+    _input(x, torch.bfloat16, (T, d), "x")
+    codes = _buffer(codes, "codes", torch.uint8, (T, d), x, stream)
+    scales = _buffer(scales, "scales", torch.uint8, (T, d // 32), x, stream)
+    with torch.cuda.device(x.device):
+        st = load_library().mk_moe_ckpt8_save(_p(x), T, d, _p(codes), _p(scales), _stream(stream))
+    _check(st, "mk_moe_ckpt8_save")
+    return codes, scales
+
+
+def mk_moe_ckpt8_dispatch(codes, scales, slot_row, x_perm=None, ws=None, stream=None):
+    """The dispatched rows from the tokens' checkpoint: x_perm[slot_row[t, j]] = token t; [T*k, d] bf16."""
+    T, d = _two_dims(codes, "codes")
+    k = _two_dims(slot_row, "slot_row")[1]
+    _input(codes, torch.uint8, (T, d), "codes")
+    _input(scales, torch.uint8, (T, d // 32), "scales", codes)
+    _input(slot_row, torch.int32, (T, k), "slot_row", codes)
+    x_perm = _buffer(x_perm, "x_perm", torch.bfloat16, (T * k, d), codes, stream)
+    ws = _workspace(ws, 256, codes, stream)
+    with torch.cuda.device(codes.device):
+        st = load_library().mk_moe_ckpt8_dispatch(_p(codes), _p(scales), _p(slot_row), T, d, k, _p(x_perm), _p(ws),
+                                                  ws.numel(), _stream(stream))
+    _check(st, "mk_moe_ckpt8_dispatch")
+    return x_perm
+
+
+def mk_moe_swiglu_ckpt8(gate, up, h=None, codes=None, scales=None, stream=None):
+    """h = silu(gate) * up on [S, f] bf16, with gate and up kept in 8 bits.
+
+    Returns (h [S, f] bf16, codes [2, S, f] uint8, scales [2, S, f / 32] uint8)."""
+    S, f = _two_dims(gate, "gate")
+    _input(gate, torch.bfloat16, (S, f), "gate")
+    _input(up, torch.bfloat16, (S, f), "up", gate)
+    h = _buffer(h, "h", torch.bfloat16, (S, f), gate, stream)
+    codes = _buffer(codes, "codes", torch.uint8, (2, S, f), gate, stream)
+    scales = _buffer(scales, "scales", torch.uint8, (2, S, f // 32), gate, stream)
+    with torch.cuda.device(gate.device):
+        st = load_library().mk_moe_swiglu_ckpt8(_p(gate), _p(up), S, f, _p(h), _p(codes), _p(scales),
+                                                _stream(stream))
+    _check(st, "mk_moe_swiglu_ckpt8")
+    return h, codes, scales
+
+
+def mk_moe_swiglu_ckpt8_bwd(dh, codes, scales, row_weight=None, dgate=None, dup=None, hw=None, drow_weight=None,
+                            stream=None):
+    """SwiGLU's backward pass from its 8-bit checkpoint.
+
+    dh [S, f] bf16 is the gradient of the rows' unweighted activations (dP @ w2), row_weight [S]
+    fp32 their routing weights (None = 1).  Returns (dgate, dup, hw [S, f] bf16, drow_weight [S]
+    fp32): hw the weighted activation that w2's gradient multiplies."""
+    S, f = _two_dims(dh, "dh")
+    _input(dh, torch.bfloat16, (S, f), "dh")
+    _input(codes, torch.uint8, (2, S, f), "codes", dh)
+    _input(scales, torch.uint8, (2, S, f // 32), "scales", dh)
+    if row_weight is not None:
+        _input(row_weight, torch.float32, (S,), "row_weight", dh)
+    dgate = _buffer(dgate, "dgate", torch.bfloat16, (S, f), dh, stream)
+    dup = _buffer(dup, "dup", torch.bfloat16, (S, f), dh, stream)
+    hw = _buffer(hw, "hw", torch.bfloat16, (S, f), dh, stream)
+    drow_weight = _buffer(drow_weight, "drow_weight", torch.float32, (S,), dh, stream)
+    with torch.cuda.device(dh.device):
+        st = load_library().mk_moe_swiglu_ckpt8_bwd(_p(dh), _p(codes), _p(scales), _p(row_weight), S, f, _p(dgate),
+                                                    _p(dup), _p(hw), _p(drow_weight), _stream(stream))
+    _check(st, "mk_moe_swiglu_ckpt8_bwd")
+    return dgate, dup, hw, drow_weight
+
+
+def _norm_input(x):
+    T, d = _two_dims(x, "x")
+    if x.dtype not in _TYPES:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    _input(x, x.dtype, (T, d), "x")
+    return T, d
+
+
+def mk_moe_layernorm(x, gamma, beta, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm over x's rows: x [T, d] bf16 or fp32, gamma and beta [d] fp32.
+
+    Returns (y [T, d] bf16, mean [T] fp32, rstd [T] fp32)."""
+    T, d = _norm_input(x)
+    _input(gamma, torch.float32, (d,), "gamma", x)
+    _input(beta, torch.float32, (d,), "beta", x)
+    y = _buffer(y, "y", torch.bfloat16, (T, d), x, stream)
+    mean = _buffer(mean, "mean", torch.float32, (T,), x, stream)
+    rstd = _buffer(rstd, "rstd", torch.float32, (T,), x, stream)
+    with torch.cuda.device(x.device):
+        st = load_library().mk_moe_layernorm(_p(x), _TYPES[x.dtype], _p(gamma), _p(beta), T, d, float(eps), _p(y),
+                                             _p(mean), _p(rstd), _stream(stream))
+    _check(st, "mk_moe_layernorm")
+    return y, mean, rstd
+
+
+def mk_moe_layernorm_bwd(dy, x, gamma, mean, rstd, dres=None, dx=None, dgamma=None, dbeta=None, ws=None, stream=None):
+    """Layer norm's backward pass: returns (dx [T, d] in x's type, dgamma [d] fp32, dbeta [d] fp32).
+
+    dres: an optional gradient [T, d] in x's type that reaches x past the norm, added into dx."""
+    T, d = _norm_input(x)
+    _input(dy, torch.bfloat16, (T, d), "dy", x)
+    _input(gamma, torch.float32, (d,), "gamma", x)
+    _input(mean, torch.float32, (T,), "mean", x)
+    _input(rstd, torch.float32, (T,), "rstd", x)
+    if dres is not None:
+        _input(dres, x.dtype, (T, d), "dres", x)
+    dx = _buffer(dx, "dx", x.dtype, (T, d), x, stream)
+    dgamma = _buffer(dgamma, "dgamma", torch.float32, (d,), x, stream)
+    dbeta = _buffer(dbeta, "dbeta", torch.float32, (d,), x, stream)
+    ws = _workspace(ws, int(load_library().mk_moe_layernorm_bwd_workspace_size(T, d)), x, stream)
+    with torch.cuda.device(x.device):
+        st = load_library().mk_moe_layernorm_bwd(_p(dy), _p(x), _TYPES[x.dtype], _p(gamma), _p(mean), _p(rstd),
+                                                 _p(dres), T, d, _p(dx), _p(dgamma), _p(dbeta), _p(ws), ws.numel(),
+                                                 _stream(stream))
+    _check(st, "mk_moe_layernorm_bwd")
+    return dx, dgamma, dbeta

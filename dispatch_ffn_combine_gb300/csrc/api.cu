@@ -320,6 +320,39 @@ mk_status mk_moe_grouped_gemm(const void* x_perm, const int32_t* expert_offsets,
     return MK_OK;
 }
 
+mk_status mk_moe_grouped_dgrad(const void* dout, const int32_t* expert_offsets, const void* w, const void* dout2,
+                               const void* w2, int64_t S, int d, int E, int n, void* dx, void* ws, size_t ws_bytes,
+                               void* stream) {
+    mk_status st = check_sizes(S, d, E, 1, n);
+    if (st != MK_OK) return st;
+    if (S == 0) return MK_OK;
+    if (!dout || !expert_offsets || !w || !dx || (dout2 == nullptr) != (w2 == nullptr)) return MK_ERR_INVALID_ARG;
+    if (!aligned16(dout) || !aligned16(w) || !aligned16(dx)) return MK_ERR_INVALID_ARG;
+    if (!aligned16(dout2) || !aligned16(w2)) return MK_ERR_INVALID_ARG;
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < 256 + 4 * (size_t(E) + 1))
+        return MK_ERR_WORKSPACE;
+    if ((st = device_ok()) != MK_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DgradArgs a;
+    a.dout = static_cast<const bf16*>(dout);
+    a.w = static_cast<const bf16*>(w);
+    a.dout2 = static_cast<const bf16*>(dout2);
+    a.w2 = static_cast<const bf16*>(w2);
+    a.offsets = expert_offsets;
+    a.mtile_start = at<int32_t>(ws, 256);
+    a.S = S;
+    a.d = d;
+    a.E = E;
+    a.n = n;
+    a.dx = static_cast<bf16*>(dx);
+    a.status = at<uint32_t>(ws, 0);
+    a.ticket = a.status + 4;
+    MK_TRY(cudaMemsetAsync(a.status, 0, 32, s));  // status, site, tile ticket
+    MK_TRY(launch_mtile_table(expert_offsets, E, S, at<int32_t>(ws, 256), a.status, s));
+    MK_TRY(launch_grouped_dgrad(a, s));
+    return MK_OK;
+}
+
 mk_status mk_moe_combine(const void* P, const int32_t* slot_row, int64_t T, int d, int k, void* y, void* stream) {
     mk_status st = check_sizes(T, d, k, k, 64);
     if (st != MK_OK) return st;

@@ -24,6 +24,14 @@
 //               accumulated over K in the same order (the tests check that the
 //               bits agree).  gemm1 keeps its blocks of 129-255 rows as full
 //               tiles when K < 4096 (kSwapMaxRowsShortK).
+//   input gradient  MODE 2, dx = dout W (+ dout2 W2): the GEMM whose sum runs
+//               over the weights' rows.  The weights [E, n, d] are read as they
+//               lie, 64 sum rows x 64 columns per box, and fed MN-major (the
+//               operand descriptor's transposed form) instead of from a
+//               transposed copy; activations, tiles, swap tiles, schedule and
+//               epilogue are gemm2's.  With two pairs of operands (gate and up)
+//               the k-blocks of the second follow those of the first into the
+//               same accumulator: one pass over dx instead of two.
 //   why         per SM and k-block, 32 KB of operands cross L2 and shared
 //               memory instead of 48 KB (B is split, not duplicated), so seven
 //               stages (3584 cycles of MMA work) fit instead of four.
@@ -126,6 +134,7 @@ struct PairParams {
     int tile_n;         // output columns per tile (128 gemm1, 256 gemm2)
     int n_valid;        // output columns of the whole GEMM
     int k_blocks;       // K / 64
+    int k_split;        // input gradient: k-blocks of the first operand pair (k_blocks if it is the only one)
     int b_rows_per_expert;
     int b_half_rows;    // row offset of CTA 1's half of B in a full tile (gemm1 0: own map; gemm2 128)
     int swap_max_rows;  // pair blocks with at most this many rows run as swap tiles (0: none)
@@ -195,13 +204,20 @@ __device__ __forceinline__ void raise_abort(PairCtl* ctl, uint32_t peer) {
     st_shared_cluster_u32(mapa_shared(smem_u32(&ctl->abort_flag), peer), 1u);
 }
 
-template <int MODE>  // 0: gemm1 + SwiGLU, 1: gemm2 + row weight
+// The second operand pair's activation rows (input gradient only), in the first one's boxes.
+struct ActMaps {
+    CUtensorMap a, a16, a32, a64;
+};
+
+constexpr uint32_t kMnBoxBytes = 64 * BK * 2;  // 64 columns of 64 weight rows
+
+template <int MODE>  // 0: gemm1 + SwiGLU, 1: gemm2 + row weight, 2: input gradient
 __global__ void __launch_bounds__(PNUM_THREADS, 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                              const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmA16,
                              const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmA64,
                              const __grid_constant__ CUtensorMap tmB0q, const __grid_constant__ CUtensorMap tmB1q,
-                             const PairParams p) {
+                             const __grid_constant__ ActMaps tmA2, const PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     PairCtl* ctl = reinterpret_cast<PairCtl*>(smem + PSTAGES * PSTAGE_BYTES);
@@ -254,6 +270,13 @@ __global__ void __launch_bounds__(PNUM_THREADS, 1)
         fence_mbar_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB0);
+        if (MODE == 2 && p.k_split < p.k_blocks) {
+            prefetch_tensormap(&tmB1);
+            prefetch_tensormap(&tmA2.a);
+            prefetch_tensormap(&tmA2.a16);
+            prefetch_tensormap(&tmA2.a32);
+            prefetch_tensormap(&tmA2.a64);
+        }
         if (MODE == 0) {
             prefetch_tensormap(&tmB1);
             prefetch_tensormap(&tmB0q);
@@ -330,12 +353,15 @@ __global__ void __launch_bounds__(PNUM_THREADS, 1)
                 int b_row = info.x * p.b_rows_per_expert + info.w + static_cast<int>(rank) * p.b_half_rows;
                 uint32_t stage_tx = PTX_BYTES;
                 const CUtensorMap* am = &tmA;
+                const CUtensorMap* am2 = &tmA2.a;
                 if (swap) {
                     // weights into the A region (gemm1: 64 output columns per CTA,
                     // gemm2: 128), this CTA's N / 2 block rows into the B region
                     const int half_n = swap_n(info.z) >> 1;
                     const int bx = swap_box(half_n);
                     am = bx == 16 ? &tmA16 : bx == 32 ? &tmA32 : bx == 64 ? &tmA64 : &tmA;
+                    if (MODE == 2)
+                        am2 = bx == 16 ? &tmA2.a16 : bx == 32 ? &tmA2.a32 : bx == 64 ? &tmA2.a64 : &tmA2.a;
                     a_row = info.y + static_cast<int>(rank) * half_n;
                     b_row = info.x * p.b_rows_per_expert + info.w +
                             static_cast<int>(rank) * (MODE == 0 ? BM / 2 : p.b_half_rows);
@@ -355,6 +381,18 @@ __global__ void __launch_bounds__(PNUM_THREADS, 1)
                         const bool stall = p.stall_first_stage && rank == 0 && cur_tile == 0 && kb == 0;
                         if (stall) {
                             // injected stall: the stage is armed but this CTA's half never comes
+                        } else if (MODE == 2) {
+                            // this CTA's 128 weight columns as two MN-major boxes of this k-block's
+                            // weight rows (columns past d read zeros)
+                            const bool second = kb >= p.k_split;
+                            const int k0 = (second ? kb - p.k_split : kb) * BK;
+                            const CUtensorMap* wm = second ? &tmB1 : &tmB0;
+                            const uint32_t sw = swap ? sa : sb;
+                            const int w_col = info.w + static_cast<int>(rank) * BM;
+                            const int w_row = info.x * p.b_rows_per_expert + k0;
+                            tma_load_2d_pair(sw, wm, w_col, w_row, fb);
+                            tma_load_2d_pair(sw + kMnBoxBytes, wm, w_col + 64, w_row, fb);
+                            tma_load_2d_pair(swap ? sb : sa, second ? am2 : am, k0, a_row, fb);
                         } else if (swap) {
                             if (MODE == 0) {
 #pragma unroll
@@ -421,7 +459,9 @@ __global__ void __launch_bounds__(PNUM_THREADS, 1)
                     slot_phase ^= 1u;
                 }
                 if (info.x < 0) break;
-                const uint32_t idesc = is_swap(info.z, p) ? idesc_bf16_f32(PAIR_M, swap_n(info.z)) : PIDESC;
+                const bool swap = is_swap(info.z, p);
+                uint32_t idesc = swap ? idesc_bf16_f32(PAIR_M, swap_n(info.z)) : PIDESC;
+                if (MODE == 2) idesc |= swap ? kIdescAMnMajor : kIdescBMnMajor;  // the weights
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_empty[acc]),
                                                                       acc_phase ^ 1u, abort_word, p.timeout_ns))) {
                     ok = false;
@@ -441,8 +481,14 @@ __global__ void __launch_bounds__(PNUM_THREADS, 1)
                         const uint32_t sb = sa + PA_BYTES;
 #pragma unroll
                         for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-                            const uint64_t ad = sw128_kmajor_desc(sa + kk * UMMA_K * 2);
-                            const uint64_t bd = sw128_kmajor_desc(sb + kk * UMMA_K * 2);
+                            uint64_t ad = sw128_kmajor_desc(sa + kk * UMMA_K * 2);
+                            uint64_t bd = sw128_kmajor_desc(sb + kk * UMMA_K * 2);
+                            if (MODE == 2) {
+                                if (swap)
+                                    ad = sw128_mnmajor_desc(sa + kk * UMMA_K * 128, kMnBoxBytes);
+                                else
+                                    bd = sw128_mnmajor_desc(sb + kk * UMMA_K * 128, kMnBoxBytes);
+                            }
                             mma_bf16_ss_pair(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
                         }
                         mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
@@ -662,7 +708,7 @@ struct PairMaps {
 };
 
 template <int MODE>
-cudaError_t launch_pair_mode(const PairMaps& m, const PairParams& p, int64_t S, cudaStream_t s) {
+cudaError_t launch_pair_mode(const PairMaps& m, const ActMaps& m2, const PairParams& p, int64_t S, cudaStream_t s) {
     static std::atomic<int> configured[64];    // per device: attributes set, max_clusters valid
     static std::atomic<int> max_clusters[64];  // written before `configured` (release / acquire)
     int dev = 0;
@@ -698,10 +744,12 @@ cudaError_t launch_pair_mode(const PairMaps& m, const PairParams& p, int64_t S, 
     const int clusters = static_cast<int>(std::min<int64_t>(resident, std::max<int64_t>(max_tiles, 1)));
     cfg.gridDim = dim3(2 * clusters);
     LaunchCfg lc(cfg.gridDim, cfg.blockDim, PSMEM_BYTES, s, p.pdl != 0, 2);
-    err = cudaLaunchKernelEx(&lc.cfg, fn, m.a, m.b0, m.b1, m.a16, m.a32, m.a64, m.b0q, m.b1q, p);
+    err = cudaLaunchKernelEx(&lc.cfg, fn, m.a, m.b0, m.b1, m.a16, m.a32, m.a64, m.b0q, m.b1q, m2, p);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
+
+const ActMaps kNoActMaps{};  // gemm1, gemm2: one operand pair
 
 }  // namespace
 
@@ -727,7 +775,7 @@ cudaError_t launch_gemm1_pair(const FfnArgs& a, cudaStream_t s) {
     p.tile_n = MMA_N / 2;
     p.n_tiles = (a.f + p.tile_n - 1) / p.tile_n;
     p.n_valid = a.f;
-    p.k_blocks = a.d / BK;
+    p.k_blocks = p.k_split = a.d / BK;
     p.b_rows_per_expert = a.f;
     p.b_half_rows = 0;  // full tiles: CTA 1 reads the same rows of W3 through its own map
     p.swap_max_rows = pair_swap_max_rows(1, p.k_blocks);
@@ -742,7 +790,7 @@ cudaError_t launch_gemm1_pair(const FfnArgs& a, cudaStream_t s) {
     p.weight_rows = nullptr;
     p.post = a.sem.h_ready;
     p.pdl = a.sem.pdl ? 1 : 0;
-    return launch_pair_mode<0>(m, p, a.S, s);
+    return launch_pair_mode<0>(m, kNoActMaps, p, a.S, s);
 }
 
 cudaError_t launch_gemm2_pair(const FfnArgs& a, cudaStream_t s) {
@@ -760,7 +808,7 @@ cudaError_t launch_gemm2_pair(const FfnArgs& a, cudaStream_t s) {
     p.tile_n = MMA_N;
     p.n_tiles = (a.d + p.tile_n - 1) / p.tile_n;
     p.n_valid = a.d;
-    p.k_blocks = a.f / BK;
+    p.k_blocks = p.k_split = a.f / BK;
     p.b_rows_per_expert = a.d;
     p.b_half_rows = MMA_N / 2;
     p.swap_max_rows = kSwapMaxRows;
@@ -775,7 +823,48 @@ cudaError_t launch_gemm2_pair(const FfnArgs& a, cudaStream_t s) {
     p.weight_rows = a.sem.mt_rows;
     p.post = a.sem.p_ready;
     p.pdl = a.sem.pdl ? 2 : 0;
-    return launch_pair_mode<1>(m, p, a.S, s);
+    return launch_pair_mode<1>(m, kNoActMaps, p, a.S, s);
+}
+
+cudaError_t launch_grouped_dgrad(const DgradArgs& a, cudaStream_t s) {
+    PairMaps m;
+    ActMaps m2 = kNoActMaps;
+    const uint64_t wrows = static_cast<uint64_t>(a.E) * a.n;
+    if (!make_act_maps(&m, a.dout, a.n, a.S) || !make_map(&m.b0, a.w, a.d, wrows, BK)) return cudaErrorInvalidValue;
+    m.b1 = m.b0q = m.b1q = m.b0;
+    if (a.dout2 != nullptr) {
+        PairMaps t;
+        if (!make_act_maps(&t, a.dout2, a.n, a.S) || !make_map(&m.b1, a.w2, a.d, wrows, BK))
+            return cudaErrorInvalidValue;
+        m2 = ActMaps{t.a, t.a16, t.a32, t.a64};
+    }
+    PairParams p;
+    p.offsets = a.offsets;
+    p.mtile_start = a.mtile_start;
+    p.row_weight = nullptr;
+    p.out = a.dx;
+    p.out_ld = a.d;
+    p.E = a.E;
+    p.tile_n = MMA_N;
+    p.n_tiles = (a.d + p.tile_n - 1) / p.tile_n;
+    p.n_valid = a.d;
+    p.k_split = a.n / BK;
+    p.k_blocks = p.k_split * (a.dout2 != nullptr ? 2 : 1);
+    p.b_rows_per_expert = a.n;
+    p.b_half_rows = 0;  // the weights' columns, not rows, are split between the CTAs
+    p.swap_max_rows = kSwapMaxRows;
+    p.status = a.status;
+    p.timeout_ns = kDefaultTimeoutNs;
+    p.stall_first_stage = 0;
+    p.ticket = a.ticket;
+    p.wait_rows = nullptr;
+    p.wait_h = nullptr;
+    p.wait_ntiles = 0;
+    p.wait_swap_max = 0;
+    p.weight_rows = nullptr;
+    p.post = nullptr;
+    p.pdl = 0;
+    return launch_pair_mode<2>(m, m2, p, a.S, s);
 }
 
 // CTA pairs when experts hold 256 rows or more on average, single CTAs below:

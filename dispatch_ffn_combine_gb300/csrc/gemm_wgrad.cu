@@ -1,0 +1,714 @@
+// gemm_wgrad.cu -- weight gradient of the grouped expert GEMM, on CTA pairs.
+//
+//   dW_e[i, j] (+)= sum over rows r of expert e of  dout[r, i] * x[r, j]
+//
+// for every expert, dout [S, n] and x [S, d] bf16 with expert e's rows
+// [off[e], off[e + 1]), fp32 accumulation, dW [E, n, d] fp32 (stored, or added
+// to what is there) or bf16 (stored).  The sum runs over an expert's rows, so
+// its length is ragged: none, one, or tens of thousands.
+//
+//   tile        256 rows of dW_e (dout columns, the M side) x 256 columns (x
+//               columns, the N side; the last tile of a row takes the 64 to
+//               192 that are left).  CTA r of the pair holds 128 dout columns
+//               and half of the x columns of a k-block of 64 rows, and its 128
+//               rows of the accumulator in its own TMEM.
+//   operands    both run along the sum's rows in memory, so both are read
+//               MN-major: a TMA box of 64 columns x 64 rows lands as 64 rows
+//               of 128 bytes (128-byte swizzle), 8 KB, two boxes per operand
+//               half; no transposed copy of either tensor is made.
+//   ragged end  an expert's last k-block holds rows of the next expert too.
+//               Only ceil(rows / 16) of its four MMA steps are issued; if the
+//               rows are no multiple of 16, a warp of each CTA first clears
+//               the foreign rows of the last step in both operands (in both,
+//               so that a NaN or infinity there is not multiplied by zero).
+//               That stage completes on a barrier of its own CTA, is cleared,
+//               and then released to the MMA warp by the two clearing warps.
+//   long sums   the tensor core's fp32 accumulator truncates, so its error grows
+//               with the number of MMA steps: over 38000 rows it was 2.5e-5 of
+//               the result's norm (1.4e-6 with rounded fp32 sums).  So a tile is
+//               summed kWChunkRows rows at a time: each chunk has a TMEM
+//               accumulator of its own, and eight epilogue warps keep the tile's
+//               sums in registers (128 each) and add the chunks in row order,
+//               rounded to nearest, while the next chunk is multiplied.
+//   order       a scheduler warp claims tiles from one ticket, experts with
+//               the most rows first, so that the last tiles are the shortest.
+//   store       the epilogue warps pass 32 x 128 bytes at a time through
+//               swizzled shared memory to TMA stores (adding: TMA reductions
+//               in L2, each element once per call, so the result does not
+//               depend on timing).  An expert without rows gets zeros.
+//
+// Every wait is bounded, as in the other pair kernels.
+#include <algorithm>
+#include <atomic>
+
+#include "gemm_impl.cuh"
+
+namespace mk {
+namespace {
+
+using namespace gemm_detail;
+
+constexpr int WSTAGES = 6;
+constexpr uint32_t WBOX_BYTES = 64 * BK * 2;             // 64 columns of 64 rows
+constexpr uint32_t WHALF_BYTES = 2 * WBOX_BYTES;         // 128 columns
+constexpr uint32_t WSTAGE_BYTES = 2 * WHALF_BYTES;       // this CTA's dout and x columns
+constexpr int kWEpiWarps = 8;                            // two per TMEM quarter, half of the columns each
+constexpr uint32_t WSTORE_BYTES = 32 * 128;              // one store of an epilogue warp
+constexpr uint32_t WSTORE_ALL = kWEpiWarps * WSTORE_BYTES;
+constexpr int kWSchedWarp = 2;
+constexpr int kWTailWarp = 3;
+constexpr int kWEpiWarp0 = 4;
+constexpr int WNUM_THREADS = 32 * (kWEpiWarp0 + kWEpiWarps);
+constexpr int kWSlots = 3;
+// Readers of a tile slot: CTA 0 its producer, MMA, tail and epilogue warps
+// plus CTA 1's relay; CTA 1 its producer, tail and epilogue warps.
+constexpr uint32_t kWSlotReaders0 = 4 + kWEpiWarps;
+constexpr uint32_t kWSlotReaders1 = 2 + kWEpiWarps;
+// Rows summed in one accumulator (a multiple of 64).  Measured on 131072 rows
+// over 64 experts of 1536 x 4096, the largest with 38360 (error of the fp32
+// gradient against 64 bits, time): 256 rows 2.7e-7, 1298 us; 512 4.7e-7, 1080;
+// 1024 9.2e-7, 1039; 2048 1.8e-6, 1035; all rows in one 2.5e-5.
+constexpr int kWChunkRows = 768;
+constexpr int kWGroupM = 8;  // M tiles walked together: tiles claimed together share operand columns in L2
+
+struct WgradCtl {
+    uint64_t full[WSTAGES];   // CTA 0: the stage is complete in both CTAs
+    uint64_t tail[WSTAGES];   // each CTA: its copies of a ragged last k-block landed
+    uint64_t empty[WSTAGES];  // each CTA: the MMAs that read the stage are done
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];  // CTA 0: both CTAs' epilogue warps have read the accumulator
+    uint64_t drain;
+    uint64_t slot_full[kWSlots];
+    uint64_t slot_empty[kWSlots];
+    int4 slot[kWSlots];  // {expert (< 0 ends the list), first row, rows, kLastChunk | m tile << 15 | n tile}
+    uint32_t tmem_base;
+    uint32_t abort_flag;
+    uint32_t zero;
+    int32_t offsets[kMaxExperts + 1];
+    uint16_t order[kMaxExperts];  // experts by falling row count
+};
+
+static_assert(WNUM_THREADS > kMaxExperts, "the prologue has a thread per offset");
+constexpr size_t WSMEM_BYTES = static_cast<size_t>(WSTAGES) * WSTAGE_BYTES + WSTORE_ALL + sizeof(WgradCtl) + 1024;
+static_assert(WSMEM_BYTES <= 227u * 1024u, "weight-gradient shared memory exceeds the per-CTA limit");
+
+struct WgradParams {
+    const int32_t* offsets;  // [E + 1]
+    int64_t S;
+    int E, n, d;
+    int m_tiles, n_tiles;
+    int accumulate;
+    uint32_t* status;
+    uint32_t* ticket;
+    uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ uint32_t wgrad_idesc(int N) {
+    return idesc_bf16_f32(PAIR_M, static_cast<uint32_t>(N)) | kIdescAMnMajor | kIdescBMnMajor;
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t src) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {  // at most N stores have still to read their shared memory
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void raise_abort(WgradCtl* ctl, uint32_t peer) {
+    ctl->abort_flag = 1u;
+    st_shared_cluster_u32(mapa_shared(smem_u32(&ctl->abort_flag), peer), 1u);
+}
+
+// A slot reader's position in the ring.
+struct SlotCursor {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == kWSlots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// The next tile of the list, for a whole warp: false if the wait ran out.
+__device__ __forceinline__ bool take_slot(WgradCtl* ctl, SlotCursor& cur, int4& info, const volatile uint32_t* abort_word,
+                                          uint64_t timeout_ns) {
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_full[cur.slot]), cur.phase, abort_word,
+                                                           timeout_ns)))
+        return false;
+    info = ctl->slot[cur.slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ctl->slot_empty[cur.slot]));
+    cur.next();
+    return true;
+}
+
+struct StageCursor {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == WSTAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void skip(int n) {
+        const uint32_t s = stage + static_cast<uint32_t>(n);
+        phase ^= (s / WSTAGES) & 1u;
+        stage = s % WSTAGES;
+    }
+};
+
+// A chunk's place in its expert's gradient, as packed in a tile slot.
+constexpr int kLastChunk = 1 << 30;
+__device__ __forceinline__ int slot_m(int w) { return (w >> 15) & 0x7fff; }
+__device__ __forceinline__ int slot_n(int w) { return w & 0x7fff; }
+
+__device__ __forceinline__ int k_blocks_of(int rows) { return (rows + BK - 1) / BK; }
+__device__ __forceinline__ int tile_cols(int n_tile, const WgradParams& p) {
+    return min(MMA_N, p.d - n_tile * MMA_N);  // a multiple of 64
+}
+
+constexpr int kHalfCols = MMA_N / 2;
+
+template <bool kBf16Out>
+__global__ void __launch_bounds__(WNUM_THREADS, 1)
+    grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmOut, const WgradParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* store_smem = smem + WSTAGES * WSTAGE_BYTES;
+    WgradCtl* ctl = reinterpret_cast<WgradCtl*>(store_smem + WSTORE_ALL);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t peer = rank ^ 1u;
+
+    // The experts' offsets, checked, and the experts by falling row count
+    // (a thread per expert).
+    const int my_e = threadIdx.x;
+    if (my_e <= p.E) ctl->offsets[my_e] = p.offsets[my_e];
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < WSTAGES; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 2);
+            mbar_init(smem_u32(&ctl->tail[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&ctl->tmem_full[a]), 1);
+            mbar_init(smem_u32(&ctl->tmem_empty[a]), 2 * kWEpiWarps);
+        }
+        for (int i = 0; i < kWSlots; ++i) {
+            mbar_init(smem_u32(&ctl->slot_full[i]), 1);
+            mbar_init(smem_u32(&ctl->slot_empty[i]), rank == 0 ? kWSlotReaders0 : kWSlotReaders1);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        ctl->zero = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmOut);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    __syncthreads();
+    bool bad = false;
+    if (my_e < p.E) {
+        const int cnt = ctl->offsets[my_e + 1] - ctl->offsets[my_e];
+        bad = cnt < 0 || ctl->offsets[my_e] < 0;
+        int rank_e = 0;
+        for (int q = 0; q < p.E; ++q) {
+            const int c = ctl->offsets[q + 1] - ctl->offsets[q];
+            rank_e += (c > cnt || (c == cnt && q < my_e)) ? 1 : 0;
+        }
+        ctl->order[rank_e] = static_cast<uint16_t>(my_e);
+    }
+    if (my_e == 0) bad = bad || ctl->offsets[0] != 0 || ctl->offsets[p.E] != p.S;
+    const bool rejected = __syncthreads_or(bad ? 1 : 0) != 0;
+    if (rejected && blockIdx.x == 0 && threadIdx.x == 0) report_error(p.status, MK_ERR_BOUNDS, kSiteWgradOffsets);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any copy, commit or arrive targets them
+    tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    volatile uint32_t* abort_word = &ctl->abort_flag;
+    const volatile uint32_t* never = &ctl->zero;
+    const int tiles_per_expert = p.m_tiles * p.n_tiles;
+    const int total_tiles = rejected ? 0 : p.E * tiles_per_expert;
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer (both CTAs)
+        const bool leader = elect_one();
+        const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+        StageCursor st;
+        SlotCursor cur;
+        uint32_t issued = 0, last_par = 0, tails = 0, tail_par = 0;  // per stage; tail_par: parity of its next use
+        bool ok = true;
+        for (;;) {
+            int4 info;
+            if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
+            if (info.x < 0) break;
+            const int kb_n = k_blocks_of(info.z);
+            const int a_col = slot_m(info.w) * PAIR_M + static_cast<int>(rank) * BM;
+            const int cols = tile_cols(slot_n(info.w), p);
+            const int b_col = slot_n(info.w) * MMA_N + static_cast<int>(rank) * (cols >> 1);
+            const int b_boxes = cols > 2 * 64 ? 2 : 1;
+            const uint32_t bytes = WHALF_BYTES + static_cast<uint32_t>(b_boxes) * WBOX_BYTES;
+            for (int kb = 0; kb < kb_n; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->empty[st.stage]), st.phase ^ 1u,
+                                                                      abort_word, p.timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                const bool ragged = kb == kb_n - 1 && (info.z & 15) != 0;
+                if (leader) {
+                    const uint32_t sa = smem_u32(smem + st.stage * WSTAGE_BYTES);
+                    const uint32_t sb = sa + WHALF_BYTES;
+                    const int row = info.y + kb * BK;
+                    uint32_t bar;
+                    if (ragged) {
+                        mbar_arrive_expect_tx(smem_u32(&ctl->tail[st.stage]), bytes);
+                        bar = mapa_shared(smem_u32(&ctl->tail[st.stage]), rank);
+                    } else {
+                        bar = full0 + st.stage * 8u;
+                        if (rank == 0) {
+                            mbar_expect_tx(smem_u32(&ctl->full[st.stage]), 2 * bytes);
+                            mbar_arrive_n(smem_u32(&ctl->full[st.stage]), 2);
+                        }
+                    }
+                    tma_load_2d_pair(sa, &tmA, a_col, row, bar);
+                    tma_load_2d_pair(sa + WBOX_BYTES, &tmA, a_col + 64, row, bar);
+                    tma_load_2d_pair(sb, &tmB, b_col, row, bar);
+                    if (b_boxes == 2) tma_load_2d_pair(sb + WBOX_BYTES, &tmB, b_col + 64, row, bar);
+                }
+                __syncwarp();
+                if (ragged) {
+                    tails |= 1u << st.stage;
+                    tail_par ^= 1u << st.stage;
+                }
+                if (rank == 0) {  // a ragged stage completes `full` too, by the tail warps' arrivals
+                    issued |= 1u << st.stage;
+                    last_par = (last_par & ~(1u << st.stage)) | (st.phase << st.stage);
+                }
+                st.next();
+            }
+            if (!ok) break;
+        }
+        if (leader) {
+            if (!ok) {
+                raise_abort(ctl, peer);
+                report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
+            }
+            // every stage armed here completes (or times out) before the CTA exits
+            for (int s = 0; s < WSTAGES; ++s) {
+                if ((issued >> s) & 1u)
+                    mbar_wait_bounded_cluster(smem_u32(&ctl->full[s]), (last_par >> s) & 1u, never, p.timeout_ns);
+                if ((tails >> s) & 1u)
+                    mbar_wait_bounded_cluster(smem_u32(&ctl->tail[s]), ((tail_par >> s) & 1u) ^ 1u, never,
+                                              p.timeout_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ------------------------------------------------ MMA issuer (CTA 0 only)
+            const bool leader = elect_one();
+            StageCursor st;
+            SlotCursor cur;
+            uint32_t acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (;;) {
+                int4 info;
+                if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
+                if (info.x < 0) break;
+                if (info.z == 0) continue;
+                const uint32_t idesc = wgrad_idesc(tile_cols(slot_n(info.w), p));
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_empty[acc]),
+                                                                      acc_phase ^ 1u, abort_word, p.timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * MMA_N;
+                const int kb_n = k_blocks_of(info.z);
+                for (int kb = 0; kb < kb_n; ++kb) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->full[st.stage]), st.phase,
+                                                                          abort_word, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t sa = smem_u32(smem + st.stage * WSTAGE_BYTES);
+                        const uint32_t sb = sa + WHALF_BYTES;
+                        const int steps = (min(BK, info.z - kb * BK) + UMMA_K - 1) / UMMA_K;
+#pragma unroll
+                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                            if (kk < steps)
+                                mma_bf16_ss_pair(d_tmem, sw128_mnmajor_desc(sa + kk * UMMA_K * 128, WBOX_BYTES),
+                                                 sw128_mnmajor_desc(sb + kk * UMMA_K * 128, WBOX_BYTES), idesc,
+                                                 (kb | kk) != 0 ? 1u : 0u);
+                        mma_commit_pair_mc(smem_u32(&ctl->empty[st.stage]), 0x3);
+                    }
+                    __syncwarp();
+                    st.next();
+                }
+                if (!ok) break;
+                if (leader) mma_commit_pair_mc(smem_u32(&ctl->tmem_full[acc]), 0x3);
+                __syncwarp();
+                acc ^= 1u;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (leader) {
+                if (!ok) {
+                    raise_abort(ctl, peer);
+                    report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmMma);
+                }
+                // All MMAs issued complete before either CTA frees TMEM or shared memory.
+                mma_commit_pair_mc(smem_u32(&ctl->drain), 0x1);
+                if (!mbar_wait_bounded_cluster(smem_u32(&ctl->drain), 0u, never, p.timeout_ns))
+                    report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmDrain);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWTailWarp) {
+        // ---------------------------------------------------- ragged last k-blocks (both CTAs)
+        const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+        StageCursor st;
+        SlotCursor cur;
+        uint32_t tail_par = 0;
+        bool ok = true;
+        for (;;) {
+            int4 info;
+            if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
+            if (info.x < 0) break;
+            const int kb_n = k_blocks_of(info.z);
+            if ((info.z & 15) == 0) {
+                st.skip(kb_n);
+                continue;
+            }
+            st.skip(kb_n - 1);
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait_bounded_cluster(smem_u32(&ctl->tail[st.stage]), (tail_par >> st.stage) & 1u,
+                                                      abort_word, p.timeout_ns))) {
+                ok = false;
+                break;
+            }
+            tail_par ^= 1u << st.stage;
+            // rows [rem, the next multiple of 16) of the four boxes (a box not loaded holds
+            // finished data that no MMA reads): whole 128-byte rows, so the swizzle does not matter
+            const int rem = info.z - (kb_n - 1) * BK;
+            const int end = (rem + UMMA_K - 1) / UMMA_K * UMMA_K;
+            uint8_t* base = smem + st.stage * WSTAGE_BYTES;
+            for (int i = lane; i < (end - rem) * 32; i += 32) {
+                const int piece = i & 7, box = (i >> 3) & 3, row = rem + (i >> 5);
+                *reinterpret_cast<uint4*>(base + box * WBOX_BYTES + row * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(full0 + st.stage * 8u);
+            st.next();
+        }
+        if (!ok && lane == 0) {
+            raise_abort(ctl, peer);
+            report_error(p.status, MK_ERR_TIMEOUT, kSiteWgradTail);
+        }
+        __syncwarp();
+    } else if (warp == kWSchedWarp) {
+        const bool leader = elect_one();
+        const int lead = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
+        SlotCursor cur;
+        bool ok = true;
+        if (rank == 0) {
+            // ------------------------------------------------ tile scheduler (CTA 0)
+            const uint32_t peer_slot0 = mapa_shared(smem_u32(&ctl->slot[0]), peer);
+            const uint32_t peer_slot_full0 = mapa_shared(smem_u32(&ctl->slot_full[0]), peer);
+            int4 nfo = make_int4(0, 0, 0, 0);
+            int row_end = 0;  // of the tile's expert
+            for (;;) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_empty[cur.slot]),
+                                                                      cur.phase ^ 1u, abort_word, p.timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                if (nfo.y + nfo.z < row_end) {  // the tile's next chunk, in this cluster too
+                    nfo.y += nfo.z;
+                    nfo.z = min(kWChunkRows, row_end - nfo.y);
+                } else {
+                    uint32_t tk = 0;
+                    if (leader) tk = atomicAdd(p.ticket, 1u);
+                    tk = __shfl_sync(0xffffffffu, tk, lead);
+                    nfo = make_int4(-1, 0, 0, 0);
+                    row_end = 0;
+                    if (tk < static_cast<uint32_t>(total_tiles)) {
+                        const int e = ctl->order[tk / tiles_per_expert];
+                        const int l = tk % tiles_per_expert;
+                        const int q = l / (kWGroupM * p.n_tiles);  // group of M tiles, walked M first
+                        const int gm = min(kWGroupM, p.m_tiles - q * kWGroupM);
+                        const int r = l - q * kWGroupM * p.n_tiles;
+                        row_end = ctl->offsets[e + 1];
+                        nfo = make_int4(e, ctl->offsets[e], min(kWChunkRows, row_end - ctl->offsets[e]),
+                                        ((q * kWGroupM + r % gm) << 15) | (r / gm));
+                    }
+                }
+                if (nfo.y + nfo.z >= row_end) nfo.w |= kLastChunk;
+                if (leader) {
+                    ctl->slot[cur.slot] = nfo;
+                    st_shared_cluster_v4(peer_slot0 + cur.slot * static_cast<uint32_t>(sizeof(int4)), nfo);
+                    mbar_arrive(smem_u32(&ctl->slot_full[cur.slot]));
+                    mbar_arrive_cluster(peer_slot_full0 + cur.slot * 8u);
+                }
+                __syncwarp();
+                cur.next();
+                if (nfo.x < 0) break;
+            }
+        } else {
+            // ------------------------------------------------ slot-release relay (CTA 1)
+            const uint32_t slot_empty0 = mapa_shared(smem_u32(&ctl->slot_empty[0]), 0);
+            for (;;) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_empty[cur.slot]), cur.phase,
+                                                                      abort_word, p.timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                const int e = ctl->slot[cur.slot].x;
+                __syncwarp();
+                if (leader) mbar_arrive_cluster(slot_empty0 + cur.slot * 8u);
+                cur.next();
+                if (e < 0) break;
+            }
+        }
+        if (!ok && leader) {
+            raise_abort(ctl, peer);
+            report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- epilogue (both CTAs, warps 4-11)
+        const int sub = warp & 3;            // TMEM lanes [32 sub, 32 sub + 32) are this warp's
+        const int half = (warp - kWEpiWarp0) >> 2;  // and columns [128 half, 128 half + 128)
+        const uint32_t tmem_empty0 = mapa_shared(smem_u32(&ctl->tmem_empty[0]), 0);
+        const uint32_t buf = smem_u32(store_smem + (warp - kWEpiWarp0) * WSTORE_BYTES);
+        SlotCursor cur;
+        uint32_t acc = 0, acc_phase = 0;
+        bool ok = true, first = true;
+        float sum[kHalfCols];
+        for (;;) {
+            int4 info;
+            if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
+            if (info.x < 0) break;
+            if (first) {
+#pragma unroll
+                for (int i = 0; i < kHalfCols; ++i) sum[i] = 0.0f;
+            }
+            if (info.z != 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_full[acc]), acc_phase,
+                                                                      abort_word, p.timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // the chunk joins the tile's sums, then its accumulator is free
+                const uint32_t tbase =
+                    tmem_base + (static_cast<uint32_t>(sub * 32) << 16) + acc * MMA_N + half * kHalfCols;
+#pragma unroll
+                for (int c = 0; c < kHalfCols; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(tbase + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[c + i] += __uint_as_float(v[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tmem_empty0 + acc * 8u);
+                acc ^= 1u;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            first = (info.w & kLastChunk) != 0;
+            if (!first) continue;
+            const int m_row = slot_m(info.w) * PAIR_M + static_cast<int>(rank) * BM + sub * 32;
+            if (m_row >= p.n || (info.z == 0 && p.accumulate)) continue;  // n is a multiple of 64: all 32 rows or none
+            const int cols = tile_cols(slot_n(info.w), p) - half * kHalfCols;
+            const int col0 = slot_n(info.w) * MMA_N + half * kHalfCols;
+            const int out_row = info.x * p.n + m_row;
+            constexpr int kCols = kBf16Out ? 64 : 32;  // columns per 128-byte row of a store
+            const uint32_t buf_row = buf + lane * 128 + (lane & 7) * 16;
+#pragma unroll
+            for (int c = 0; c < kHalfCols; c += kCols) {
+                if (c >= cols) break;
+                if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint4 o;
+                    if (kBf16Out)
+                        o = make_uint4(pack_bf16x2(sum[c + 8 * q], sum[c + 8 * q + 1]),
+                                       pack_bf16x2(sum[c + 8 * q + 2], sum[c + 8 * q + 3]),
+                                       pack_bf16x2(sum[c + 8 * q + 4], sum[c + 8 * q + 5]),
+                                       pack_bf16x2(sum[c + 8 * q + 6], sum[c + 8 * q + 7]));
+                    else
+                        o = make_uint4(__float_as_uint(sum[c + 4 * q]), __float_as_uint(sum[c + 4 * q + 1]),
+                                       __float_as_uint(sum[c + 4 * q + 2]), __float_as_uint(sum[c + 4 * q + 3]));
+                    st_shared_v4(buf_row ^ (q * 16), o);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (!kBf16Out && p.accumulate)
+                        tma_reduce_add_2d(&tmOut, col0 + c, out_row, buf);
+                    else
+                        tma_store_2d(&tmOut, col0 + c, out_row, buf);
+                    bulk_commit();
+                }
+            }
+        }
+        if (lane == 0) {
+            bulk_wait_all();
+            if (!ok) {
+                raise_abort(ctl, peer);
+                report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmEpilogue);
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA leaves while the other may still use its shared memory
+    if (*abort_word != 0u && threadIdx.x == 0) {
+        // After a timeout, copies the peer started may still complete on this CTA's
+        // barriers: keep both CTAs resident a little longer (bounded) before exit.
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+// 2-D row-major tensor [rows, inner], box {box_cols, box_rows} of 128-byte rows, 128-byte swizzle.
+bool make_map_box(CUtensorMap* m, const void* base, bool fp32, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const uint32_t size = fp32 ? 4 : 2;
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {inner * size};
+    const cuuint32_t box[2] = {128u / size, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kBf16Out>
+cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const WgradParams& p,
+                         cudaStream_t s) {
+    static std::atomic<int> max_clusters[64];  // per device, 0 until configured
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    auto fn = grouped_wgrad_kernel<kBf16Out>;
+    LaunchCfg lc(dim3(2 * std::max(1, device_sm_count() / 2)), dim3(WNUM_THREADS), WSMEM_BYTES, s, false, 2);
+    int n = dev < 64 ? max_clusters[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(WSMEM_BYTES));
+        if (err != cudaSuccess) return err;
+        err = cudaOccupancyMaxActiveClusters(&n, fn, &lc.cfg);
+        if (err != cudaSuccess) return err;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        if (dev < 64) max_clusters[dev].store(n, std::memory_order_release);
+    }
+    const int64_t tiles = static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles;
+    lc.cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(n, tiles)));
+    err = cudaLaunchKernelEx(&lc.cfg, fn, a, b, out, p);
+    if (err != cudaSuccess) return err;
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* expert_offsets, const void* x_perm,
+                                          int64_t S, int d, int E, int n, void* dw, int dw_type, int accumulate,
+                                          void* ws, size_t ws_bytes, void* stream) {
+    const mk_status st = check_sizes(S, d, E, 1, n);
+    if (st != MK_OK) return st;
+    const int64_t m_tiles = (n + PAIR_M - 1) / PAIR_M, n_tiles = (d + MMA_N - 1) / MMA_N;
+    if (m_tiles > 0x7fff || n_tiles > 0x7fff || m_tiles * n_tiles * E >= (int64_t(1) << 31)) return MK_ERR_UNSUPPORTED;
+    if (dw_type != MK_TYPE_BF16 && dw_type != MK_TYPE_FP32) return MK_ERR_INVALID_ARG;
+    if (accumulate && dw_type != MK_TYPE_FP32) return MK_ERR_INVALID_ARG;
+    if (!dw || !aligned16(dw)) return MK_ERR_INVALID_ARG;
+    if (S > 0 && (!dout || !expert_offsets || !x_perm || !aligned16(dout) || !aligned16(x_perm)))
+        return MK_ERR_INVALID_ARG;
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < 256) return MK_ERR_WORKSPACE;
+    if (!device_is_sm103()) return MK_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint32_t* status = static_cast<uint32_t*>(ws);
+    if (cudaMemsetAsync(status, 0, 32, s) != cudaSuccess) return MK_ERR_CUDA;  // status, site, tile ticket
+    const bool fp32 = dw_type == MK_TYPE_FP32;
+    if (S == 0) {  // no rows: every expert's gradient is zero
+        if (!accumulate &&
+            cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * n * d * (fp32 ? 4 : 2), s) != cudaSuccess)
+            return MK_ERR_CUDA;
+        return MK_OK;
+    }
+    CUtensorMap a, b, out;
+    if (!make_map_box(&a, dout, false, n, S, BK) || !make_map_box(&b, x_perm, false, d, S, BK) ||
+        !make_map_box(&out, dw, fp32, d, static_cast<uint64_t>(E) * n, 32))
+        return MK_ERR_CUDA;
+    WgradParams p;
+    p.offsets = expert_offsets;
+    p.S = S;
+    p.E = E;
+    p.n = n;
+    p.d = d;
+    p.m_tiles = static_cast<int>(m_tiles);
+    p.n_tiles = static_cast<int>(n_tiles);
+    p.accumulate = accumulate ? 1 : 0;
+    p.status = status;
+    p.ticket = status + 4;
+    p.timeout_ns = kDefaultTimeoutNs;
+    const cudaError_t err = fp32 ? launch_wgrad<false>(a, b, out, p, s) : launch_wgrad<true>(a, b, out, p, s);
+    return err == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}

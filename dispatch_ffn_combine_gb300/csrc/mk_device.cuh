@@ -178,6 +178,17 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -199,6 +210,24 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
     desc |= static_cast<uint64_t>(2u) << 61;
     return desc;
 }
+
+// Shared-memory matrix descriptor for an MN-major bf16 operand (the sum's index
+// is the slow one in memory): per sum row 64 MN elements (128 bytes) with the
+// 128-byte swizzle, 8-row groups 1024 bytes apart (stride offset), the next 64
+// MN elements `box_bytes` further (leading offset): the layout that TMA boxes
+// {64, rows} with SWIZZLE_128B write.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t box_bytes) {
+    uint64_t desc = 0;
+    desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    desc |= static_cast<uint64_t>(box_bytes >> 4) << 16;
+    desc |= static_cast<uint64_t>(1024u >> 4) << 32;
+    desc |= static_cast<uint64_t>(1u) << 46;
+    desc |= static_cast<uint64_t>(2u) << 61;
+    return desc;
+}
+
+constexpr uint32_t kIdescAMnMajor = 1u << 15;  // instruction descriptor: A (B) is MN-major
+constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major, M x N.
 //   bits 4-5 D format (1 = f32), bits 7-9 A format (1 = bf16), bits 10-12 B

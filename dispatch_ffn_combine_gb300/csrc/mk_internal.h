@@ -31,6 +31,9 @@ enum : uint32_t {
     kSiteFusedIdle = 0x800,
     kSiteCombineWait = 0x900,
     kSiteRegroup = 0xA00,
+    kSiteCkptSlot = 0xB00,
+    kSiteWgradOffsets = 0xC00,
+    kSiteWgradTail = 0xD00,
 };
 
 // Byte offsets of every region of the caller's workspace.  The first 256
@@ -196,6 +199,22 @@ struct FfnArgs {
     int64_t gather_T = 0;
     const int32_t* row_token = nullptr;
 };
+// Input gradient of the grouped GEMM: dx = dout W_e (+ dout2 W2_e), on CTA
+// pairs (gemm_pair.cu).  dout, dout2 [S, n]; w, w2 [E, n, d]; dx [S, d].
+struct DgradArgs {
+    const bf16* dout;
+    const bf16* w;
+    const bf16* dout2;  // null: one operand pair
+    const bf16* w2;
+    const int32_t* offsets;      // [E+1]
+    const int32_t* mtile_start;  // [E+1]
+    int64_t S;
+    int d, E, n;
+    bf16* dx;
+    uint32_t* status;
+    uint32_t* ticket;  // a zeroed word
+};
+cudaError_t launch_grouped_dgrad(const DgradArgs& a, cudaStream_t s);
 // The pair kernels' swap-tile thresholds (gemm2's combine readiness needs it).
 int pair_swap_max_rows(int gemm, int k_blocks);
 bool use_pairs(const FfnArgs& a);

@@ -401,6 +401,113 @@ typedef enum {
 MK_API mk_status mk_moe_workspace_region(int64_t T, int d, int E, int k, int ffn, int region, size_t* offset,
                                          size_t* bytes);
 
+/* ------------------------------------------------------------------ training
+ *
+ * What a training step needs beside the forward steps above.  The pages
+ * describe an inference layer only; these are additions of this library.  A
+ * step of the layer with the experts' weights as [E, out, in]:
+ *
+ *   forward   mk_moe_layernorm; mk_moe_route; mk_moe_dispatch; gate, up =
+ *             mk_moe_grouped_gemm(x_perm, w1 | w3); mk_moe_swiglu_ckpt8; P =
+ *             mk_moe_grouped_gemm(h, w2, row_weight); mk_moe_combine.  Kept:
+ *             the routing tables, mk_moe_ckpt8_save(x), SwiGLU's checkpoint.
+ *   backward  dP = mk_moe_dispatch(dy); dh = mk_moe_grouped_dgrad(dP, w2);
+ *             mk_moe_swiglu_ckpt8_bwd; dw2 = mk_moe_grouped_wgrad(dP, hw);
+ *             x_perm = mk_moe_ckpt8_dispatch; dw1, dw3 =
+ *             mk_moe_grouped_wgrad(dgate | dup, x_perm); dx_perm =
+ *             mk_moe_grouped_dgrad(dgate, w1, dup, w3); dx =
+ *             mk_moe_combine(dx_perm); mk_moe_layernorm_bwd.
+ *
+ * The conventions at the top of this file hold; results repeat bit for bit. */
+
+#define MK_TYPE_BF16 0
+#define MK_TYPE_FP32 1
+
+/* Input gradient of the grouped GEMM, on the tensor cores:
+ *   dx[r] = bf16( dout[r] W_e (+ dout2[r] W2_e) )   (fp32 accumulate)
+ * for every row r of expert e: the gradient of mk_moe_grouped_gemm's x_perm,
+ * or, with both operand pairs, that of rows that went through two weights
+ * (gate and up).
+ *   dout bf16 [S, n]; expert_offsets int32 [E+1] with off[0] = 0, off[E] = S
+ *   w    bf16 [E, n, d], as in the forward call
+ *   dout2 [S, n] and w2 [E, n, d]: both given or both NULL
+ *   dx   bf16 [S, d] (out)
+ *   ws: at least 256 + 4 (E + 1) bytes.
+ * Limits and bad offsets as in mk_moe_grouped_gemm. */
+MK_API mk_status mk_moe_grouped_dgrad(const void* dout, const int32_t* expert_offsets, const void* w,
+                               const void* dout2, const void* w2, int64_t S, int d, int E, int n, void* dx,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* Weight gradient of the grouped GEMM, on the tensor cores:
+ *   dw[e] (+)= sum over rows r of expert e of dout[r]^T x_perm[r]   (fp32 accumulate)
+ *   dout bf16 [S, n]; x_perm bf16 [S, d]; expert_offsets as above
+ *   dw   [E, n, d] (out): dw_type MK_TYPE_FP32 or MK_TYPE_BF16.  accumulate != 0
+ *        (fp32 only) adds to dw; otherwise dw is overwritten, with zeros for an
+ *        expert without rows (and for all of them when S == 0).
+ *   ws: at least 256 bytes.
+ * Rows of one expert never reach another's gradient, NaN and infinities
+ * included.  Bad offsets set MK_ERR_BOUNDS on the device and dw is untouched. */
+MK_API mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* expert_offsets, const void* x_perm,
+                               int64_t S, int d, int E, int n, void* dw, int dw_type, int accumulate,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* Tokens kept in 8 bits for the backward pass: every value one e4m3 code,
+ * every block of 32 consecutive values one scale byte b, the value code *
+ * 2^(b - 127).  The scale is the smallest power of two (2^-124 at least) that
+ * brings the block's largest finite magnitude to 448 or below; codes round to
+ * nearest even; NaN and infinities become NaN, and finite values stay finite
+ * (magnitudes above 1.875 * 2^127 become that).
+ *   x bf16 [T, d]; codes uint8 [T, d] (out, 16-byte aligned); scales uint8 [T, d / 32] (out)
+ * Limits: d a multiple of 64, T < 2^31, T * d < 2^40. */
+MK_API mk_status mk_moe_ckpt8_save(const void* x, int64_t T, int d, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The dispatched rows again, from the tokens' checkpoint:
+ *   x_perm[slot_row[t, j]] = the value of token t   (exact in bf16)
+ *   slot_row int32 [T, k] as mk_moe_dispatch wrote it; x_perm bf16 [T*k, d] (out)
+ *   ws: at least 256 bytes.  A row index outside [0, T*k) sets MK_ERR_BOUNDS on
+ * the device and is skipped.  Limits: 1 <= k <= 8, T * k < 2^31, T * k * d < 2^40. */
+MK_API mk_status mk_moe_ckpt8_dispatch(const uint8_t* codes, const uint8_t* scales, const int32_t* slot_row, int64_t T,
+                                int d, int k, void* x_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* SwiGLU that keeps its inputs in 8 bits: h = bf16( silu(gate) * up ), and the
+ * codes and scales of gate (first plane) and up (second plane) in the format above.
+ *   gate, up bf16 [S, f]; h bf16 [S, f] (out)
+ *   codes uint8 [2, S, f] (out, 16-byte aligned); scales uint8 [2, S, f / 32] (out)
+ * Limits: f a multiple of 64, S < 2^31, S * f < 2^40. */
+MK_API mk_status mk_moe_swiglu_ckpt8(const void* gate, const void* up, int64_t S, int f, void* h, uint8_t* codes,
+                              uint8_t* scales, void* stream);
+
+/* Its backward pass from the checkpoint, with g, u the values kept, a = silu(g)
+ * and w the row's routing weight (row_weight fp32 [S], NULL = 1):
+ *   dgate = bf16( w dh u silu'(g) ), dup = bf16( w dh a ), hw = bf16( w a u ),
+ *   drow_weight[r] = sum over the row of dh a u   (fp32, one fixed order)
+ *   dh bf16 [S, f]: the gradient of the row's unweighted activation, dP W2
+ *   dgate, dup bf16 [S, f] (out); hw bf16 [S, f] and drow_weight fp32 [S] (out, may be NULL) */
+MK_API mk_status mk_moe_swiglu_ckpt8_bwd(const void* dh, const uint8_t* codes, const uint8_t* scales,
+                                  const float* row_weight, int64_t S, int f, void* dgate, void* dup, void* hw,
+                                  float* drow_weight, void* stream);
+
+/* Layer norm over rows of d values, as ahead of the layer:
+ *   mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ *   y = bf16( (x - mean) rstd gamma + beta )
+ *   x [T, d], x_type MK_TYPE_BF16 or MK_TYPE_FP32; gamma, beta fp32 [d]
+ *   y bf16 [T, d] (out); mean, rstd fp32 [T] (out), kept for the backward pass
+ * Any d from 1 to 16384 (multiples of 8, of 4 for fp32 x, are faster); eps >= 0; T < 2^31, T * d < 2^40. */
+MK_API mk_status mk_moe_layernorm(const void* x, int x_type, const float* gamma, const float* beta, int64_t T, int d,
+                           float eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace mk_moe_layernorm_bwd needs.  Returns 0 if the sizes are invalid. */
+MK_API size_t mk_moe_layernorm_bwd_workspace_size(int64_t T, int d);
+
+/* Its backward pass, with xh = (x - mean) rstd and t = dy gamma:
+ *   dx = rstd (t - sum t / d - xh sum(t xh) / d) (+ dres)   in x's type
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy   (one fixed order)
+ *   dy bf16 [T, d]; dres [T, d] in x's type or NULL: a gradient that reaches x
+ *   past the norm (the residual stream); dx [T, d] (out); dgamma, dbeta fp32 [d] (out; zeros when T == 0) */
+MK_API mk_status mk_moe_layernorm_bwd(const void* dy, const void* x, int x_type, const float* gamma,
+                               const float* mean, const float* rstd, const void* dres, int64_t T, int d, void* dx,
+                               float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 MK_API const char* mk_moe_status_string(mk_status s);
 
