@@ -492,7 +492,7 @@ MK_API mk_status mk_moe_swiglu_ckpt8_bwd(const void* dh, const uint8_t* codes, c
  *   y = bf16( (x - mean) rstd gamma + beta )
  *   x [T, d], x_type MK_TYPE_BF16 or MK_TYPE_FP32; gamma, beta fp32 [d]
  *   y bf16 [T, d] (out); mean, rstd fp32 [T] (out), kept for the backward pass
- * Any d from 1 to 16384 (multiples of 8, of 4 for fp32 x, are faster); eps >= 0; T < 2^31, T * d < 2^40. */
+ * Any d from 1 to 16384 (16376 unless a multiple of 8); eps >= 0; T < 2^31, T * d < 2^40. */
 MK_API mk_status mk_moe_layernorm(const void* x, int x_type, const float* gamma, const float* beta, int64_t T, int d,
                            float eps, void* y, float* mean, float* rstd, void* stream);
 
