@@ -517,81 +517,96 @@ def mk_moe_ep_regroup(rows_in, counts, to_expert_major, rows_out=None, expert_of
 
 
 # ----------------------------------------------------------------- training
+#
+# These calls are short on small batches (a few microseconds on the GPU), so
+# their bindings check every argument with one pass over plain attributes and
+# pass addresses as integers.
 
 MK_TYPE_BF16 = 0
 MK_TYPE_FP32 = 1
 _TYPES = {torch.bfloat16: MK_TYPE_BF16, torch.float32: MK_TYPE_FP32}
+_BF, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _buffer(t, name, dtype, shape, like, stream):
-    """`t` checked as an output or workspace on `like`'s device, or a new tensor.
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _inputs(like, *wanted):
+    """Checks (tensor or None, dtype, shape, name) each; `like` gives the device."""
+    dev = like.get_device()
+    for t, dtype, shape, name in wanted:
+        if t is None:
+            continue
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous() and dev >= 0:
+                continue
+        except AttributeError:
+            pass
+        _need(t, dtype, shape, name)  # says what is wrong
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+
+
+def _new(t, dtype, shape, like, stream):
+    """The output or workspace that was passed, or a new one.
 
     A new tensor belongs to the current stream's memory; where the call runs on
     another one, the allocator is told, so that the memory is not handed out
     again before that stream is done with it."""
     if t is not None:
-        return _same_device(_need(t, dtype, shape, name), name, like)
+        return t
     t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _same_device(t, name, like):
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return t
-
-
-def _input(t, dtype, shape, name, like=None):
-    _need(t, dtype, shape, name)
-    return t if like is None else _same_device(t, name, like)
-
-
-def _two_dims(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    return t.shape
-
-
 def _workspace(ws, nbytes, like, stream):
     if ws is None:
-        return _buffer(None, "ws", torch.uint8, (nbytes,), like, stream)
-    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous() or not ws.is_cuda:
+        return _new(None, _U8, (nbytes,), like, stream)
+    if not isinstance(ws, torch.Tensor) or ws.dtype != _U8 or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous CUDA tensor of bytes")
-    return _same_device(ws, "ws", like)
+    if ws.device != like.device:
+        raise ValueError(f"ws must be on {like.device}, got {ws.device}")
+    return ws
 
 
-def _expert_weight(w, name, n, like):
-    if not isinstance(w, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if w.dim() != 3:
-        raise ValueError(f"{name} must have 3 dimensions, got {w.dim()}")
-    E, _, d = w.shape
-    _input(w, torch.bfloat16, (E, n, d), name, like)
-    return E, d
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(name, like, stream, *args):
+    """The library call `name` on `stream` (None: the current one) of `like`'s device."""
+    dev = like.get_device()
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    fn = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != MK_OK:
+        raise MoEError(st, name)
 
 
 def mk_moe_grouped_dgrad(dout, expert_offsets, w, dout2=None, w2=None, dx=None, ws=None, stream=None):
     """Input gradient of the grouped GEMM: dx[r] = dout[r] @ w[e] (+ dout2[r] @ w2[e]) for the
     rows r of expert e.  dout, dout2 [S, n] and w, w2 [E, n, d] bf16; returns dx [S, d] bf16."""
-    S, n = _two_dims(dout, "dout")
-    _input(dout, torch.bfloat16, (S, n), "dout")
-    E, d = _expert_weight(w, "w", n, dout)
-    _input(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dout)
+    S, n = _dims(dout, "dout", 2)
+    E, _, d = _dims(w, "w", 3)
     if (dout2 is None) != (w2 is None):
         raise ValueError("dout2 and w2 go together")
-    if dout2 is not None:
-        _input(dout2, torch.bfloat16, (S, n), "dout2", dout)
-        _input(w2, torch.bfloat16, (E, n, d), "w2", dout)
-    dx = _buffer(dx, "dx", torch.bfloat16, (S, d), dout, stream)
+    _inputs(dout, (dout, _BF, (S, n), "dout"), (w, _BF, (E, n, d), "w"),
+            (expert_offsets, _I32, (E + 1,), "expert_offsets"), (dout2, _BF, (S, n), "dout2"),
+            (w2, _BF, (E, n, d), "w2"), (dx, _BF, (S, d), "dx"))
+    dx = _new(dx, _BF, (S, d), dout, stream)
     ws = _workspace(ws, 256 + 4 * (E + 1), dout, stream)
-    with torch.cuda.device(dout.device):
-        st = load_library().mk_moe_grouped_dgrad(_p(dout), _p(expert_offsets), _p(w), _p(dout2), _p(w2), S, d, E, n,
-                                                 _p(dx), _p(ws), ws.numel(), _stream(stream))
-    _check(st, "mk_moe_grouped_dgrad")
+    _run("mk_moe_grouped_dgrad", dout, stream, dout.data_ptr(), _at(expert_offsets), w.data_ptr(), _at(dout2), _at(w2),
+         S, d, E, n, dx.data_ptr(), ws.data_ptr(), ws.numel())
     return dx
 
 
@@ -602,54 +617,45 @@ def mk_moe_grouped_wgrad(dout, expert_offsets, x_perm, dw=None, accumulate=False
     dout [S, n] and x_perm [S, d] bf16; returns dw [E, n, d] in `dtype` (fp32 or bf16; the passed
     dw's own type when there is one).  accumulate adds to the passed fp32 dw; otherwise dw is
     overwritten (zeros for an expert without rows)."""
-    S, n = _two_dims(dout, "dout")
-    _input(dout, torch.bfloat16, (S, n), "dout")
-    d = _two_dims(x_perm, "x_perm")[1]
-    _input(x_perm, torch.bfloat16, (S, d), "x_perm", dout)
-    if not isinstance(expert_offsets, torch.Tensor) or expert_offsets.dim() != 1 or expert_offsets.numel() < 2:
-        raise ValueError("expert_offsets must be a 1-D tensor of E + 1 row offsets")
-    E = expert_offsets.numel() - 1
-    _input(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dout)
+    S, n = _dims(dout, "dout", 2)
+    d = _dims(x_perm, "x_perm", 2)[1]
+    E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
+    if E < 1:
+        raise ValueError("expert_offsets must hold E + 1 row offsets")
     dtype = dw.dtype if isinstance(dw, torch.Tensor) else dtype
     if dtype not in _TYPES:
         raise TypeError(f"dw must be torch.float32 or torch.bfloat16, got {dtype}")
-    if accumulate and (dw is None or dtype != torch.float32):
+    if accumulate and (dw is None or dtype != _F32):
         raise ValueError("accumulate needs an fp32 dw to add to")
-    dw = _buffer(dw, "dw", dtype, (E, n, d), dout, stream)
+    _inputs(dout, (dout, _BF, (S, n), "dout"), (x_perm, _BF, (S, d), "x_perm"),
+            (expert_offsets, _I32, (E + 1,), "expert_offsets"), (dw, dtype, (E, n, d), "dw"))
+    dw = _new(dw, dtype, (E, n, d), dout, stream)
     ws = _workspace(ws, 256, dout, stream)
-    with torch.cuda.device(dout.device):
-        st = load_library().mk_moe_grouped_wgrad(_p(dout), _p(expert_offsets), _p(x_perm), S, d, E, n, _p(dw),
-                                                 _TYPES[dtype], 1 if accumulate else 0, _p(ws), ws.numel(),
-                                                 _stream(stream))
-    _check(st, "mk_moe_grouped_wgrad")
+    _run("mk_moe_grouped_wgrad", dout, stream, dout.data_ptr(), expert_offsets.data_ptr(), x_perm.data_ptr(), S, d, E,
+         n, dw.data_ptr(), _TYPES[dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel())
     return dw
 
 
 def mk_moe_ckpt8_save(x, codes=None, scales=None, stream=None):
     """Tokens x [T, d] bf16 kept in 8 bits: returns (codes [T, d] uint8, scales [T, d / 32] uint8)."""
-    T, d = _two_dims(x, "x")
-    _input(x, torch.bfloat16, (T, d), "x")
-    codes = _buffer(codes, "codes", torch.uint8, (T, d), x, stream)
-    scales = _buffer(scales, "scales", torch.uint8, (T, d // 32), x, stream)
-    with torch.cuda.device(x.device):
-        st = load_library().mk_moe_ckpt8_save(_p(x), T, d, _p(codes), _p(scales), _stream(stream))
-    _check(st, "mk_moe_ckpt8_save")
+    T, d = _dims(x, "x", 2)
+    _inputs(x, (x, _BF, (T, d), "x"), (codes, _U8, (T, d), "codes"), (scales, _U8, (T, d // 32), "scales"))
+    codes = _new(codes, _U8, (T, d), x, stream)
+    scales = _new(scales, _U8, (T, d // 32), x, stream)
+    _run("mk_moe_ckpt8_save", x, stream, x.data_ptr(), T, d, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def mk_moe_ckpt8_dispatch(codes, scales, slot_row, x_perm=None, ws=None, stream=None):
     """The dispatched rows from the tokens' checkpoint: x_perm[slot_row[t, j]] = token t; [T*k, d] bf16."""
-    T, d = _two_dims(codes, "codes")
-    k = _two_dims(slot_row, "slot_row")[1]
-    _input(codes, torch.uint8, (T, d), "codes")
-    _input(scales, torch.uint8, (T, d // 32), "scales", codes)
-    _input(slot_row, torch.int32, (T, k), "slot_row", codes)
-    x_perm = _buffer(x_perm, "x_perm", torch.bfloat16, (T * k, d), codes, stream)
+    T, d = _dims(codes, "codes", 2)
+    k = _dims(slot_row, "slot_row", 2)[1]
+    _inputs(codes, (codes, _U8, (T, d), "codes"), (scales, _U8, (T, d // 32), "scales"),
+            (slot_row, _I32, (T, k), "slot_row"), (x_perm, _BF, (T * k, d), "x_perm"))
+    x_perm = _new(x_perm, _BF, (T * k, d), codes, stream)
     ws = _workspace(ws, 256, codes, stream)
-    with torch.cuda.device(codes.device):
-        st = load_library().mk_moe_ckpt8_dispatch(_p(codes), _p(scales), _p(slot_row), T, d, k, _p(x_perm), _p(ws),
-                                                  ws.numel(), _stream(stream))
-    _check(st, "mk_moe_ckpt8_dispatch")
+    _run("mk_moe_ckpt8_dispatch", codes, stream, codes.data_ptr(), _at(scales), slot_row.data_ptr(), T, d, k,
+         x_perm.data_ptr(), ws.data_ptr(), ws.numel())
     return x_perm
 
 
@@ -657,16 +663,14 @@ def mk_moe_swiglu_ckpt8(gate, up, h=None, codes=None, scales=None, stream=None):
     """h = silu(gate) * up on [S, f] bf16, with gate and up kept in 8 bits.
 
     Returns (h [S, f] bf16, codes [2, S, f] uint8, scales [2, S, f / 32] uint8)."""
-    S, f = _two_dims(gate, "gate")
-    _input(gate, torch.bfloat16, (S, f), "gate")
-    _input(up, torch.bfloat16, (S, f), "up", gate)
-    h = _buffer(h, "h", torch.bfloat16, (S, f), gate, stream)
-    codes = _buffer(codes, "codes", torch.uint8, (2, S, f), gate, stream)
-    scales = _buffer(scales, "scales", torch.uint8, (2, S, f // 32), gate, stream)
-    with torch.cuda.device(gate.device):
-        st = load_library().mk_moe_swiglu_ckpt8(_p(gate), _p(up), S, f, _p(h), _p(codes), _p(scales),
-                                                _stream(stream))
-    _check(st, "mk_moe_swiglu_ckpt8")
+    S, f = _dims(gate, "gate", 2)
+    _inputs(gate, (gate, _BF, (S, f), "gate"), (up, _BF, (S, f), "up"), (h, _BF, (S, f), "h"),
+            (codes, _U8, (2, S, f), "codes"), (scales, _U8, (2, S, f // 32), "scales"))
+    h = _new(h, _BF, (S, f), gate, stream)
+    codes = _new(codes, _U8, (2, S, f), gate, stream)
+    scales = _new(scales, _U8, (2, S, f // 32), gate, stream)
+    _run("mk_moe_swiglu_ckpt8", gate, stream, gate.data_ptr(), _at(up), S, f, h.data_ptr(), codes.data_ptr(),
+         scales.data_ptr())
     return h, codes, scales
 
 
@@ -677,28 +681,23 @@ def mk_moe_swiglu_ckpt8_bwd(dh, codes, scales, row_weight=None, dgate=None, dup=
     dh [S, f] bf16 is the gradient of the rows' unweighted activations (dP @ w2), row_weight [S]
     fp32 their routing weights (None = 1).  Returns (dgate, dup, hw [S, f] bf16, drow_weight [S]
     fp32): hw the weighted activation that w2's gradient multiplies."""
-    S, f = _two_dims(dh, "dh")
-    _input(dh, torch.bfloat16, (S, f), "dh")
-    _input(codes, torch.uint8, (2, S, f), "codes", dh)
-    _input(scales, torch.uint8, (2, S, f // 32), "scales", dh)
-    if row_weight is not None:
-        _input(row_weight, torch.float32, (S,), "row_weight", dh)
-    dgate = _buffer(dgate, "dgate", torch.bfloat16, (S, f), dh, stream)
-    dup = _buffer(dup, "dup", torch.bfloat16, (S, f), dh, stream)
-    hw = _buffer(hw, "hw", torch.bfloat16, (S, f), dh, stream)
-    drow_weight = _buffer(drow_weight, "drow_weight", torch.float32, (S,), dh, stream)
-    with torch.cuda.device(dh.device):
-        st = load_library().mk_moe_swiglu_ckpt8_bwd(_p(dh), _p(codes), _p(scales), _p(row_weight), S, f, _p(dgate),
-                                                    _p(dup), _p(hw), _p(drow_weight), _stream(stream))
-    _check(st, "mk_moe_swiglu_ckpt8_bwd")
+    S, f = _dims(dh, "dh", 2)
+    _inputs(dh, (dh, _BF, (S, f), "dh"), (codes, _U8, (2, S, f), "codes"), (scales, _U8, (2, S, f // 32), "scales"),
+            (row_weight, _F32, (S,), "row_weight"), (dgate, _BF, (S, f), "dgate"), (dup, _BF, (S, f), "dup"),
+            (hw, _BF, (S, f), "hw"), (drow_weight, _F32, (S,), "drow_weight"))
+    dgate = _new(dgate, _BF, (S, f), dh, stream)
+    dup = _new(dup, _BF, (S, f), dh, stream)
+    hw = _new(hw, _BF, (S, f), dh, stream)
+    drow_weight = _new(drow_weight, _F32, (S,), dh, stream)
+    _run("mk_moe_swiglu_ckpt8_bwd", dh, stream, dh.data_ptr(), _at(codes), _at(scales), _at(row_weight), S, f,
+         dgate.data_ptr(), dup.data_ptr(), hw.data_ptr(), drow_weight.data_ptr())
     return dgate, dup, hw, drow_weight
 
 
-def _norm_input(x):
-    T, d = _two_dims(x, "x")
+def _norm_rows(x):
+    T, d = _dims(x, "x", 2)
     if x.dtype not in _TYPES:
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
-    _input(x, x.dtype, (T, d), "x")
     return T, d
 
 
@@ -706,16 +705,14 @@ def mk_moe_layernorm(x, gamma, beta, eps=1e-5, y=None, mean=None, rstd=None, str
     """Layer norm over x's rows: x [T, d] bf16 or fp32, gamma and beta [d] fp32.
 
     Returns (y [T, d] bf16, mean [T] fp32, rstd [T] fp32)."""
-    T, d = _norm_input(x)
-    _input(gamma, torch.float32, (d,), "gamma", x)
-    _input(beta, torch.float32, (d,), "beta", x)
-    y = _buffer(y, "y", torch.bfloat16, (T, d), x, stream)
-    mean = _buffer(mean, "mean", torch.float32, (T,), x, stream)
-    rstd = _buffer(rstd, "rstd", torch.float32, (T,), x, stream)
-    with torch.cuda.device(x.device):
-        st = load_library().mk_moe_layernorm(_p(x), _TYPES[x.dtype], _p(gamma), _p(beta), T, d, float(eps), _p(y),
-                                             _p(mean), _p(rstd), _stream(stream))
-    _check(st, "mk_moe_layernorm")
+    T, d = _norm_rows(x)
+    _inputs(x, (x, x.dtype, (T, d), "x"), (gamma, _F32, (d,), "gamma"), (beta, _F32, (d,), "beta"),
+            (y, _BF, (T, d), "y"), (mean, _F32, (T,), "mean"), (rstd, _F32, (T,), "rstd"))
+    y = _new(y, _BF, (T, d), x, stream)
+    mean = _new(mean, _F32, (T,), x, stream)
+    rstd = _new(rstd, _F32, (T,), x, stream)
+    _run("mk_moe_layernorm", x, stream, x.data_ptr(), _TYPES[x.dtype], _at(gamma), _at(beta), T, d, float(eps),
+         y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
 
 
@@ -723,20 +720,15 @@ def mk_moe_layernorm_bwd(dy, x, gamma, mean, rstd, dres=None, dx=None, dgamma=No
     """Layer norm's backward pass: returns (dx [T, d] in x's type, dgamma [d] fp32, dbeta [d] fp32).
 
     dres: an optional gradient [T, d] in x's type that reaches x past the norm, added into dx."""
-    T, d = _norm_input(x)
-    _input(dy, torch.bfloat16, (T, d), "dy", x)
-    _input(gamma, torch.float32, (d,), "gamma", x)
-    _input(mean, torch.float32, (T,), "mean", x)
-    _input(rstd, torch.float32, (T,), "rstd", x)
-    if dres is not None:
-        _input(dres, x.dtype, (T, d), "dres", x)
-    dx = _buffer(dx, "dx", x.dtype, (T, d), x, stream)
-    dgamma = _buffer(dgamma, "dgamma", torch.float32, (d,), x, stream)
-    dbeta = _buffer(dbeta, "dbeta", torch.float32, (d,), x, stream)
-    ws = _workspace(ws, int(load_library().mk_moe_layernorm_bwd_workspace_size(T, d)), x, stream)
-    with torch.cuda.device(x.device):
-        st = load_library().mk_moe_layernorm_bwd(_p(dy), _p(x), _TYPES[x.dtype], _p(gamma), _p(mean), _p(rstd),
-                                                 _p(dres), T, d, _p(dx), _p(dgamma), _p(dbeta), _p(ws), ws.numel(),
-                                                 _stream(stream))
-    _check(st, "mk_moe_layernorm_bwd")
+    T, d = _norm_rows(x)
+    _inputs(x, (dy, _BF, (T, d), "dy"), (x, x.dtype, (T, d), "x"), (gamma, _F32, (d,), "gamma"),
+            (mean, _F32, (T,), "mean"), (rstd, _F32, (T,), "rstd"), (dres, x.dtype, (T, d), "dres"),
+            (dx, x.dtype, (T, d), "dx"), (dgamma, _F32, (d,), "dgamma"), (dbeta, _F32, (d,), "dbeta"))
+    dx = _new(dx, x.dtype, (T, d), x, stream)
+    dgamma = _new(dgamma, _F32, (d,), x, stream)
+    dbeta = _new(dbeta, _F32, (d,), x, stream)
+    nbytes = (_lib or load_library()).mk_moe_layernorm_bwd_workspace_size(T, d)
+    ws = _workspace(ws, nbytes, x, stream)
+    _run("mk_moe_layernorm_bwd", x, stream, _at(dy), x.data_ptr(), _TYPES[x.dtype], _at(gamma), _at(mean), _at(rstd),
+         _at(dres), T, d, dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel())
     return dx, dgamma, dbeta

@@ -195,11 +195,31 @@ struct Place {
             if (has(v, 2 * e + 1)) store1(p + 2 * e + 1, f[e].y());
         }
     }
-    __device__ __forceinline__ void weights(const float* w, int v, f2 (&f)[4]) const {  // zeros outside the row
+    // The weights of vector v, zeros outside the row.  Away from the row's ends they are read
+    // as the aligned words around them and shifted into place.
+    __device__ __forceinline__ void weights(const float* w, int v, f2 (&f)[4]) const {
+        const int c = col + kLaneStep * v;
+        const int sh = kAligned ? 0 : c & 3;
+        if (kAligned ? in(v) : c - sh >= 0 && c - sh + 12 <= col + left) {
+            float q[12];
+#pragma unroll
+            for (int i = 0; i < (kAligned ? 2 : 3); ++i) {
+                const float4 t = __ldg(reinterpret_cast<const float4*>(w + (c - sh)) + i);
+                q[4 * i] = t.x, q[4 * i + 1] = t.y, q[4 * i + 2] = t.z, q[4 * i + 3] = t.w;
+            }
+            if (!kAligned) {
+#pragma unroll
+                for (int i = 0; i < 11; ++i) q[i] = (sh & 1) ? q[i + 1] : q[i];
+#pragma unroll
+                for (int i = 0; i < 9; ++i) q[i] = (sh & 2) ? q[i + 2] : q[i];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = f2(q[2 * e], q[2 * e + 1]);
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            f[e] = f2(has(v, 2 * e) ? __ldg(w + col + kLaneStep * v + 2 * e) : 0.0f,
-                      has(v, 2 * e + 1) ? __ldg(w + col + kLaneStep * v + 2 * e + 1) : 0.0f);
+            f[e] = f2(has(v, 2 * e) ? __ldg(w + c + 2 * e) : 0.0f, has(v, 2 * e + 1) ? __ldg(w + c + 2 * e + 1) : 0.0f);
     }
 };
 
@@ -453,7 +473,7 @@ struct RowShape {
 // measurements.  Forward, 4 vectors share a thread's fixed work per row (sums,
 // copies) best (32768 x 7168 bf16: 155 us, with 2 vectors 232); backward, the
 // columns' sums of 4 vectors do not fit the registers (307 us, with 2 262).
-RowShape row_shape(int d, bool forward) {
+RowShape row_shape(int64_t rows, int d, bool forward) {
     const int n = d % 8 == 0 ? d : d + 7;  // the row's words may start up to 7 values before it
     RowShape best{};
     double most = 0.0;
@@ -470,6 +490,8 @@ RowShape row_shape(int d, bool forward) {
             best = s;
         }
     }
+    // few rows: spread over all SMs
+    best.rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(best.rows, (rows + device_sm_count() - 1) / device_sm_count())));
     return best;
 }
 
@@ -541,7 +563,7 @@ cudaError_t launch_fwd(const NormArgs& a, RowShape r) {
 
 template <typename T>
 cudaError_t run_fwd(const NormArgs& a) {
-    const RowShape r = row_shape(a.d, true);
+    const RowShape r = row_shape(a.rows, a.d, true);
     return r.nv == 1 ? launch_fwd<T, 1>(a, r) : r.nv == 2 ? launch_fwd<T, 2>(a, r) : launch_fwd<T, 4>(a, r);
 }
 
@@ -560,7 +582,7 @@ cudaError_t launch_bwd(NormArgs& a, const RowShape& r, const Ring& q) {
 
 template <typename T>
 cudaError_t run_bwd(NormArgs& a) {
-    RowShape r = row_shape(a.d, false);
+    RowShape r = row_shape(a.rows, a.d, false);
     const int xs = a.dres != nullptr ? 2 : 1;
     const Ring q = ring_shape(r, r.nv * (RingPart<T, 1>::kWords * xs + RingPart<bf16, 1>::kWords));
     if (q.stages == 1) return launch_bwd<T, 4, 1>(a, r, q);  // fp32 rows of over 11000 values with dres
