@@ -39,12 +39,13 @@ ENTRY_POINTS = (
     "mk_moe_grouped_gemm", "mk_moe_dispatch_gemm_workspace_size", "mk_moe_dispatch_gemm",
     "mk_moe_route_approx_logits", "mk_moe_workspace_region", "mk_moe_ep_regroup_workspace_size",
     "mk_moe_ep_regroup",
-    "mk_moe_grouped_dgrad", "mk_moe_grouped_wgrad", "mk_moe_ckpt8_save", "mk_moe_ckpt8_dispatch",
+    "mk_moe_grouped_dgrad", "mk_moe_grouped_wgrad_workspace_size", "mk_moe_grouped_wgrad",
+    "mk_moe_ckpt8_save", "mk_moe_ckpt8_dispatch",
     "mk_moe_swiglu_ckpt8", "mk_moe_swiglu_ckpt8_bwd", "mk_moe_layernorm", "mk_moe_layernorm_bwd_workspace_size",
     "mk_moe_layernorm_bwd",
 )
 _SIZE_RESULT = ("mk_moe_workspace_size", "mk_moe_dispatch_gemm_workspace_size", "mk_moe_ep_regroup_workspace_size",
-                "mk_moe_layernorm_bwd_workspace_size")
+                "mk_moe_layernorm_bwd_workspace_size", "mk_moe_grouped_wgrad_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -107,6 +108,8 @@ def load_library():
         lib.mk_moe_ep_regroup.argtypes = [P, P, P, I, I, I64, I, I, P, P, SZ, P]
         F = ctypes.c_float
         lib.mk_moe_grouped_dgrad.argtypes = [P, P, P, P, P, I64, I, I, I, P, P, SZ, P]
+        lib.mk_moe_grouped_wgrad_workspace_size.restype = SZ
+        lib.mk_moe_grouped_wgrad_workspace_size.argtypes = [I64, I, I, I]
         lib.mk_moe_grouped_wgrad.argtypes = [P, P, P, I64, I, I, I, P, I, I, P, SZ, P]
         lib.mk_moe_ckpt8_save.argtypes = [P, I64, I, P, P, P]
         lib.mk_moe_ckpt8_dispatch.argtypes = [P, P, P, I64, I, I, P, P, SZ, P]
@@ -630,6 +633,9 @@ def mk_moe_grouped_wgrad(dout, expert_offsets, x_perm, dw=None, accumulate=False
     _inputs(dout, (dout, _BF, (S, n), "dout"), (x_perm, _BF, (S, d), "x_perm"),
             (expert_offsets, _I32, (E + 1,), "expert_offsets"), (dw, dtype, (E, n, d), "dw"))
     dw = _new(dw, dtype, (E, n, d), dout, stream)
+    if ws is None:
+        nbytes = (_lib or load_library()).mk_moe_grouped_wgrad_workspace_size(S, d, E, n)
+        ws = _new(None, _U8, (max(nbytes, 256),), dout, stream)
     ws = _workspace(ws, 256, dout, stream)
     _run("mk_moe_grouped_wgrad", dout, stream, dout.data_ptr(), expert_offsets.data_ptr(), x_perm.data_ptr(), S, d, E,
          n, dw.data_ptr(), _TYPES[dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel())

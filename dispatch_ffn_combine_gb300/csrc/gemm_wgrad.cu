@@ -17,12 +17,14 @@
 //               of 128 bytes (128-byte swizzle), 8 KB, two boxes per operand
 //               half; no transposed copy of either tensor is made.
 //   ragged end  an expert's last k-block holds rows of the next expert too.
-//               Only ceil(rows / 16) of its four MMA steps are issued; if the
-//               rows are no multiple of 16, a warp of each CTA first clears
-//               the foreign rows of the last step in both operands (in both,
-//               so that a NaN or infinity there is not multiplied by zero).
-//               That stage completes on a barrier of its own CTA, is cleared,
-//               and then released to the MMA warp by the two clearing warps.
+//               Only its own rows are loaded, in boxes of 32, 16, 8, 4, 2 and 1
+//               rows, and the last MMA step of 16 rows is filled up with boxes
+//               past the tensor's end, which read as zeros: both operands are
+//               zero there, so that a NaN of the next expert is not multiplied
+//               by zero.  (The 128-byte swizzle follows the shared-memory
+//               address, so boxes of any height make up one tile.  Clearing the
+//               foreign rows with a warp after the copy cost 5 to 25 % at 8
+//               k-blocks per tile.)
 //   long sums   the tensor core's fp32 accumulator truncates, so its error grows
 //               with the number of MMA steps: over 38000 rows it was 2.5e-5 of
 //               the result's norm (1.4e-6 with rounded fp32 sums).  So a tile is
@@ -30,6 +32,11 @@
 //               accumulator of its own, and eight epilogue warps keep the tile's
 //               sums in registers (128 each) and add the chunks in row order,
 //               rounded to nearest, while the next chunk is multiplied.
+//   few tiles   where the tiles do not fill the GPU, an expert's rows are cut
+//               into pieces; each piece's tiles are a sum of their own, stored
+//               to the workspace, and a second kernel adds an expert's pieces
+//               in row order.  (131072 rows of one 64 x 64 expert: 535 us as one
+//               tile.)
 //   order       a scheduler warp claims tiles from one ticket, experts with
 //               the most rows first, so that the last tiles are the shortest.
 //   store       the epilogue warps pass 32 x 128 bytes at a time through
@@ -56,41 +63,53 @@ constexpr int kWEpiWarps = 8;                            // two per TMEM quarter
 constexpr uint32_t WSTORE_BYTES = 32 * 128;              // one store of an epilogue warp
 constexpr uint32_t WSTORE_ALL = kWEpiWarps * WSTORE_BYTES;
 constexpr int kWSchedWarp = 2;
-constexpr int kWTailWarp = 3;
-constexpr int kWEpiWarp0 = 4;
+constexpr int kWEpiWarp0 = 4;  // registers move between warpgroups; warp 3 only fills up the first
 constexpr int WNUM_THREADS = 32 * (kWEpiWarp0 + kWEpiWarps);
-constexpr int kWSlots = 3;
-// Readers of a tile slot: CTA 0 its producer, MMA, tail and epilogue warps
-// plus CTA 1's relay; CTA 1 its producer, tail and epilogue warps.
-constexpr uint32_t kWSlotReaders0 = 4 + kWEpiWarps;
+constexpr int kWSlots = 8;  // most tiles claimed ahead
+// Readers of a tile slot: CTA 0 its producer, MMA and epilogue warps plus CTA
+// 1's slot relay; CTA 1 its producer, accumulator relay and epilogue warps.
+constexpr uint32_t kWSlotReaders0 = 3 + kWEpiWarps;
 constexpr uint32_t kWSlotReaders1 = 2 + kWEpiWarps;
 // Rows summed in one accumulator (a multiple of 64).  Measured on 131072 rows
 // over 64 experts of 1536 x 4096, the largest with 38360 (error of the fp32
 // gradient against 64 bits, time): 256 rows 2.7e-7, 1298 us; 512 4.7e-7, 1080;
 // 1024 9.2e-7, 1039; 2048 1.8e-6, 1035; all rows in one 2.5e-5.
 constexpr int kWChunkRows = 768;
+// A tile's four (bf16: two) stores per epilogue warp are spread over the next
+// tile's main loop, this many SM cycles per k-block of the last chunk apart:
+// bursts of stores hold up the operand loads.  Measured (32 experts of about
+// 512 rows, 1408 x 2048 fp32): 0: 116 us, 100: 115, 200: 107, 300: 130; 64
+// experts of 2048 x 7168 bf16 with 1024 rows: 1262, 1232, 1217, 1199 us.
+constexpr int kStorePace = 200;
+constexpr int kClusters = 76;  // what the splitting and pacing rules assume resident
 constexpr int kWGroupM = 8;  // M tiles walked together: tiles claimed together share operand columns in L2
 
 struct WgradCtl {
-    uint64_t full[WSTAGES];   // CTA 0: the stage is complete in both CTAs
-    uint64_t tail[WSTAGES];   // each CTA: its copies of a ragged last k-block landed
+    uint64_t full[WSTAGES];   // CTA 0: both CTAs' copies of the stage landed
     uint64_t empty[WSTAGES];  // each CTA: the MMAs that read the stage are done
     uint64_t tmem_full[2];
-    uint64_t tmem_empty[2];  // CTA 0: both CTAs' epilogue warps have read the accumulator
+    uint64_t tmem_empty[2];  // each CTA: its epilogue warps have read the accumulator (CTA 0: and CTA 1's)
+    // the accumulator
     uint64_t drain;
     uint64_t slot_full[kWSlots];
     uint64_t slot_empty[kWSlots];
-    int4 slot[kWSlots];  // {expert (< 0 ends the list), first row, rows, kLastChunk | m tile << 15 | n tile}
+    int4 slot[kWSlots];  // {expert or piece (< 0 ends the list), first row, rows, kLastChunk | m tile << 15 | n tile}
     uint32_t tmem_base;
     uint32_t abort_flag;
     uint32_t zero;
     int32_t offsets[kMaxExperts + 1];
-    uint16_t order[kMaxExperts];  // experts by falling row count
+    uint16_t index[kMaxExperts + 1];  // experts by falling row count; split sums: prefix over experts of their pieces
 };
 
 static_assert(WNUM_THREADS > kMaxExperts, "the prologue has a thread per offset");
 constexpr size_t WSMEM_BYTES = static_cast<size_t>(WSTAGES) * WSTAGE_BYTES + WSTORE_ALL + sizeof(WgradCtl) + 1024;
 static_assert(WSMEM_BYTES <= 227u * 1024u, "weight-gradient shared memory exceeds the per-CTA limit");
+
+// One operand [S, columns] in boxes of 64 columns x 64, 32, 16, 8, 4, 2 and 1 rows.
+constexpr int kBoxes = 7;
+struct OperandMaps {
+    CUtensorMap m[kBoxes];
+};
 
 struct WgradParams {
     const int32_t* offsets;  // [E + 1]
@@ -98,6 +117,9 @@ struct WgradParams {
     int E, n, d;
     int m_tiles, n_tiles;
     int accumulate;
+    int pace;         // cycles per k-block between the stores of a tile
+    int split_rows;   // 0, or the most rows of a piece (a multiple of 64)
+    int slots, batch;  // tiles claimed ahead (<= kWSlots), and at a time
     uint32_t* status;
     uint32_t* ticket;
     uint64_t timeout_ns;
@@ -105,14 +127,6 @@ struct WgradParams {
 
 __device__ __forceinline__ uint32_t wgrad_idesc(int N) {
     return idesc_bf16_f32(PAIR_M, static_cast<uint32_t>(N)) | kIdescAMnMajor | kIdescBMnMajor;
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async_shared() {
@@ -153,8 +167,8 @@ __device__ __forceinline__ void raise_abort(WgradCtl* ctl, uint32_t peer) {
 // A slot reader's position in the ring.
 struct SlotCursor {
     uint32_t slot = 0, phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == kWSlots) {
+    __device__ __forceinline__ void next(int slots) {
+        if (static_cast<int>(++slot) == slots) {
             slot = 0;
             phase ^= 1u;
         }
@@ -163,14 +177,14 @@ struct SlotCursor {
 
 // The next tile of the list, for a whole warp: false if the wait ran out.
 __device__ __forceinline__ bool take_slot(WgradCtl* ctl, SlotCursor& cur, int4& info, const volatile uint32_t* abort_word,
-                                          uint64_t timeout_ns) {
+                                          const WgradParams& p) {
     if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_full[cur.slot]), cur.phase, abort_word,
-                                                           timeout_ns)))
+                                                           p.timeout_ns)))
         return false;
     info = ctl->slot[cur.slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ctl->slot_empty[cur.slot]));
-    cur.next();
+    cur.next(p.slots);
     return true;
 }
 
@@ -182,12 +196,11 @@ struct StageCursor {
             phase ^= 1u;
         }
     }
-    __device__ __forceinline__ void skip(int n) {
-        const uint32_t s = stage + static_cast<uint32_t>(n);
-        phase ^= (s / WSTAGES) & 1u;
-        stage = s % WSTAGES;
-    }
 };
+
+__host__ __device__ __forceinline__ int pieces_of(int rows, int split_rows) {
+    return (max(rows, 0) + split_rows - 1) / split_rows;
+}
 
 // A chunk's place in its expert's gradient, as packed in a tile slot.
 constexpr int kLastChunk = 1 << 30;
@@ -203,7 +216,7 @@ constexpr int kHalfCols = MMA_N / 2;
 
 template <bool kBf16Out>
 __global__ void __launch_bounds__(WNUM_THREADS, 1)
-    grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    grouped_wgrad_kernel(const __grid_constant__ OperandMaps tmA, const __grid_constant__ OperandMaps tmB,
                          const __grid_constant__ CUtensorMap tmOut, const WgradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -220,13 +233,12 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
     if (my_e <= p.E) ctl->offsets[my_e] = p.offsets[my_e];
     if (threadIdx.x == 0) {
         for (int s = 0; s < WSTAGES; ++s) {
-            mbar_init(smem_u32(&ctl->full[s]), 2);
-            mbar_init(smem_u32(&ctl->tail[s]), 1);
+            mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&ctl->tmem_full[a]), 1);
-            mbar_init(smem_u32(&ctl->tmem_empty[a]), 2 * kWEpiWarps);
+            mbar_init(smem_u32(&ctl->tmem_empty[a]), rank == 0 ? kWEpiWarps + 1 : kWEpiWarps);
         }
         for (int i = 0; i < kWSlots; ++i) {
             mbar_init(smem_u32(&ctl->slot_full[i]), 1);
@@ -236,8 +248,10 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
         ctl->abort_flag = 0;
         ctl->zero = 0;
         fence_mbar_init();
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
+        for (int i = 0; i < kBoxes; ++i) {
+            prefetch_tensormap(&tmA.m[i]);
+            prefetch_tensormap(&tmB.m[i]);
+        }
         prefetch_tensormap(&tmOut);
     }
     if (warp == 1) {
@@ -254,7 +268,12 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
             const int c = ctl->offsets[q + 1] - ctl->offsets[q];
             rank_e += (c > cnt || (c == cnt && q < my_e)) ? 1 : 0;
         }
-        ctl->order[rank_e] = static_cast<uint16_t>(my_e);
+        if (p.split_rows == 0) ctl->index[rank_e] = static_cast<uint16_t>(my_e);
+    }
+    if (p.split_rows != 0 && my_e <= p.E) {
+        int before = 0;
+        for (int q = 0; q < my_e; ++q) before += pieces_of(ctl->offsets[q + 1] - ctl->offsets[q], p.split_rows);
+        ctl->index[my_e] = static_cast<uint16_t>(min(before, 0xffff));  // few: fewer tiles than clusters are split
     }
     if (my_e == 0) bad = bad || ctl->offsets[0] != 0 || ctl->offsets[p.E] != p.S;
     const bool rejected = __syncthreads_or(bad ? 1 : 0) != 0;
@@ -267,274 +286,299 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
     volatile uint32_t* abort_word = &ctl->abort_flag;
     const volatile uint32_t* never = &ctl->zero;
     const int tiles_per_expert = p.m_tiles * p.n_tiles;
-    const int total_tiles = rejected ? 0 : p.E * tiles_per_expert;
+    const int total_tiles = rejected ? 0 : (p.split_rows != 0 ? ctl->index[p.E] : p.E) * tiles_per_expert;
 
-    if (warp == 0) {
-        // ---------------------------------------------------- TMA producer (both CTAs)
-        const bool leader = elect_one();
-        const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
-        StageCursor st;
-        SlotCursor cur;
-        uint32_t issued = 0, last_par = 0, tails = 0, tail_par = 0;  // per stage; tail_par: parity of its next use
-        bool ok = true;
-        for (;;) {
-            int4 info;
-            if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
-            if (info.x < 0) break;
-            const int kb_n = k_blocks_of(info.z);
-            const int a_col = slot_m(info.w) * PAIR_M + static_cast<int>(rank) * BM;
-            const int cols = tile_cols(slot_n(info.w), p);
-            const int b_col = slot_n(info.w) * MMA_N + static_cast<int>(rank) * (cols >> 1);
-            const int b_boxes = cols > 2 * 64 ? 2 : 1;
-            const uint32_t bytes = WHALF_BYTES + static_cast<uint32_t>(b_boxes) * WBOX_BYTES;
-            for (int kb = 0; kb < kb_n; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->empty[st.stage]), st.phase ^ 1u,
-                                                                      abort_word, p.timeout_ns))) {
-                    ok = false;
-                    break;
-                }
-                const bool ragged = kb == kb_n - 1 && (info.z & 15) != 0;
-                if (leader) {
-                    const uint32_t sa = smem_u32(smem + st.stage * WSTAGE_BYTES);
-                    const uint32_t sb = sa + WHALF_BYTES;
-                    const int row = info.y + kb * BK;
-                    uint32_t bar;
-                    if (ragged) {
-                        mbar_arrive_expect_tx(smem_u32(&ctl->tail[st.stage]), bytes);
-                        bar = mapa_shared(smem_u32(&ctl->tail[st.stage]), rank);
-                    } else {
-                        bar = full0 + st.stage * 8u;
-                        if (rank == 0) {
-                            mbar_expect_tx(smem_u32(&ctl->full[st.stage]), 2 * bytes);
-                            mbar_arrive_n(smem_u32(&ctl->full[st.stage]), 2);
-                        }
-                    }
-                    tma_load_2d_pair(sa, &tmA, a_col, row, bar);
-                    tma_load_2d_pair(sa + WBOX_BYTES, &tmA, a_col + 64, row, bar);
-                    tma_load_2d_pair(sb, &tmB, b_col, row, bar);
-                    if (b_boxes == 2) tma_load_2d_pair(sb + WBOX_BYTES, &tmB, b_col + 64, row, bar);
-                }
-                __syncwarp();
-                if (ragged) {
-                    tails |= 1u << st.stage;
-                    tail_par ^= 1u << st.stage;
-                }
-                if (rank == 0) {  // a ragged stage completes `full` too, by the tail warps' arrivals
-                    issued |= 1u << st.stage;
-                    last_par = (last_par & ~(1u << st.stage)) | (st.phase << st.stage);
-                }
-                st.next();
-            }
-            if (!ok) break;
-        }
-        if (leader) {
-            if (!ok) {
-                raise_abort(ctl, peer);
-                report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
-            }
-            // every stage armed here completes (or times out) before the CTA exits
-            for (int s = 0; s < WSTAGES; ++s) {
-                if ((issued >> s) & 1u)
-                    mbar_wait_bounded_cluster(smem_u32(&ctl->full[s]), (last_par >> s) & 1u, never, p.timeout_ns);
-                if ((tails >> s) & 1u)
-                    mbar_wait_bounded_cluster(smem_u32(&ctl->tail[s]), ((tail_par >> s) & 1u) ^ 1u, never,
-                                              p.timeout_ns);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0) {
-            // ------------------------------------------------ MMA issuer (CTA 0 only)
+    // The epilogue warps take the registers (their sums) that the other four give up: 64 + 2 x 216 of the
+    // 3 x 168 per warp that the block is launched with.
+    if (warp < kWEpiWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 0) {
+            // ---------------------------------------------------- TMA producer (both CTAs)
             const bool leader = elect_one();
+            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
             StageCursor st;
             SlotCursor cur;
-            uint32_t acc = 0, acc_phase = 0;
+            uint32_t issued = 0, last_par = 0;
             bool ok = true;
             for (;;) {
                 int4 info;
-                if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
+                if (!(ok = take_slot(ctl, cur, info, abort_word, p))) break;
                 if (info.x < 0) break;
-                if (info.z == 0) continue;
-                const uint32_t idesc = wgrad_idesc(tile_cols(slot_n(info.w), p));
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_empty[acc]),
-                                                                      acc_phase ^ 1u, abort_word, p.timeout_ns))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * MMA_N;
                 const int kb_n = k_blocks_of(info.z);
+                const int a_col = slot_m(info.w) * PAIR_M + static_cast<int>(rank) * BM;
+                const int cols = tile_cols(slot_n(info.w), p);
+                const int b_col = slot_n(info.w) * MMA_N + static_cast<int>(rank) * (cols >> 1);
+                const int b_boxes = cols > 2 * 64 ? 2 : 1;
                 for (int kb = 0; kb < kb_n; ++kb) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->full[st.stage]), st.phase,
-                                                                          abort_word, p.timeout_ns))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->empty[st.stage]),
+                                                                          st.phase ^ 1u, abort_word, p.timeout_ns))) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
                     if (leader) {
                         const uint32_t sa = smem_u32(smem + st.stage * WSTAGE_BYTES);
-                        const uint32_t sb = sa + WHALF_BYTES;
-                        const int steps = (min(BK, info.z - kb * BK) + UMMA_K - 1) / UMMA_K;
-#pragma unroll
-                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
-                            if (kk < steps)
-                                mma_bf16_ss_pair(d_tmem, sw128_mnmajor_desc(sa + kk * UMMA_K * 128, WBOX_BYTES),
-                                                 sw128_mnmajor_desc(sb + kk * UMMA_K * 128, WBOX_BYTES), idesc,
-                                                 (kb | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair_mc(smem_u32(&ctl->empty[st.stage]), 0x3);
+                        const uint32_t fb = full0 + st.stage * 8u;
+                        const int row = info.y + kb * BK;
+                        const int left = min(BK, info.z - kb * BK);
+                        const int filled = (left + UMMA_K - 1) / UMMA_K * UMMA_K;
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(smem_u32(&ctl->full[st.stage]),
+                                                  2u * static_cast<uint32_t>((2 + b_boxes) * filled * 128));
+                        // `h` rows from row r of both tensors to row `at` of the stage
+                        auto load = [&](int box, int at, int r) {
+                            const uint32_t a = sa + static_cast<uint32_t>(at) * 128u, b = a + WHALF_BYTES;
+                            tma_load_2d_pair(a, &tmA.m[box], a_col, r, fb);
+                            tma_load_2d_pair(a + WBOX_BYTES, &tmA.m[box], a_col + 64, r, fb);
+                            tma_load_2d_pair(b, &tmB.m[box], b_col, r, fb);
+                            if (b_boxes == 2) tma_load_2d_pair(b + WBOX_BYTES, &tmB.m[box], b_col + 64, r, fb);
+                        };
+                        if (left == BK) {
+                            load(0, 0, row);
+                        } else {
+                            int at = 0;
+#pragma unroll 1
+                            for (int box = 1; box < kBoxes; ++box)
+                                if (left & (BK >> box)) {
+                                    load(box, at, row + at);
+                                    at += BK >> box;
+                                }
+                            const int fill = filled - left;
+#pragma unroll 1
+                            for (int box = kBoxes - 1; box > 2; --box)
+                                if (fill & (BK >> box)) {
+                                    load(box, at, static_cast<int>(p.S));  // past the last row: zeros
+                                    at += BK >> box;
+                                }
+                        }
                     }
                     __syncwarp();
+                    if (rank == 0) {
+                        issued |= 1u << st.stage;
+                        last_par = (last_par & ~(1u << st.stage)) | (st.phase << st.stage);
+                    }
                     st.next();
                 }
                 if (!ok) break;
-                if (leader) mma_commit_pair_mc(smem_u32(&ctl->tmem_full[acc]), 0x3);
-                __syncwarp();
-                acc ^= 1u;
-                if (acc == 0) acc_phase ^= 1u;
             }
             if (leader) {
                 if (!ok) {
                     raise_abort(ctl, peer);
-                    report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmMma);
+                    report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
                 }
-                // All MMAs issued complete before either CTA frees TMEM or shared memory.
-                mma_commit_pair_mc(smem_u32(&ctl->drain), 0x1);
-                if (!mbar_wait_bounded_cluster(smem_u32(&ctl->drain), 0u, never, p.timeout_ns))
-                    report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmDrain);
+                // CTA 0: every stage it armed completes (or times out) before the CTA exits
+                for (int s = 0; s < WSTAGES; ++s)
+                    if ((issued >> s) & 1u)
+                        mbar_wait_bounded_cluster(smem_u32(&ctl->full[s]), (last_par >> s) & 1u, never, p.timeout_ns);
             }
-        }
-        __syncwarp();
-    } else if (warp == kWTailWarp) {
-        // ---------------------------------------------------- ragged last k-blocks (both CTAs)
-        const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
-        StageCursor st;
-        SlotCursor cur;
-        uint32_t tail_par = 0;
-        bool ok = true;
-        for (;;) {
-            int4 info;
-            if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
-            if (info.x < 0) break;
-            const int kb_n = k_blocks_of(info.z);
-            if ((info.z & 15) == 0) {
-                st.skip(kb_n);
-                continue;
-            }
-            st.skip(kb_n - 1);
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait_bounded_cluster(smem_u32(&ctl->tail[st.stage]), (tail_par >> st.stage) & 1u,
-                                                      abort_word, p.timeout_ns))) {
-                ok = false;
-                break;
-            }
-            tail_par ^= 1u << st.stage;
-            // rows [rem, the next multiple of 16) of the four boxes (a box not loaded holds
-            // finished data that no MMA reads): whole 128-byte rows, so the swizzle does not matter
-            const int rem = info.z - (kb_n - 1) * BK;
-            const int end = (rem + UMMA_K - 1) / UMMA_K * UMMA_K;
-            uint8_t* base = smem + st.stage * WSTAGE_BYTES;
-            for (int i = lane; i < (end - rem) * 32; i += 32) {
-                const int piece = i & 7, box = (i >> 3) & 3, row = rem + (i >> 5);
-                *reinterpret_cast<uint4*>(base + box * WBOX_BYTES + row * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(full0 + st.stage * 8u);
-            st.next();
-        }
-        if (!ok && lane == 0) {
-            raise_abort(ctl, peer);
-            report_error(p.status, MK_ERR_TIMEOUT, kSiteWgradTail);
-        }
-        __syncwarp();
-    } else if (warp == kWSchedWarp) {
-        const bool leader = elect_one();
-        const int lead = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
-        SlotCursor cur;
-        bool ok = true;
-        if (rank == 0) {
-            // ------------------------------------------------ tile scheduler (CTA 0)
-            const uint32_t peer_slot0 = mapa_shared(smem_u32(&ctl->slot[0]), peer);
-            const uint32_t peer_slot_full0 = mapa_shared(smem_u32(&ctl->slot_full[0]), peer);
-            int4 nfo = make_int4(0, 0, 0, 0);
-            int row_end = 0;  // of the tile's expert
-            for (;;) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_empty[cur.slot]),
-                                                                      cur.phase ^ 1u, abort_word, p.timeout_ns))) {
-                    ok = false;
-                    break;
-                }
-                if (nfo.y + nfo.z < row_end) {  // the tile's next chunk, in this cluster too
-                    nfo.y += nfo.z;
-                    nfo.z = min(kWChunkRows, row_end - nfo.y);
-                } else {
-                    uint32_t tk = 0;
-                    if (leader) tk = atomicAdd(p.ticket, 1u);
-                    tk = __shfl_sync(0xffffffffu, tk, lead);
-                    nfo = make_int4(-1, 0, 0, 0);
-                    row_end = 0;
-                    if (tk < static_cast<uint32_t>(total_tiles)) {
-                        const int e = ctl->order[tk / tiles_per_expert];
-                        const int l = tk % tiles_per_expert;
-                        const int q = l / (kWGroupM * p.n_tiles);  // group of M tiles, walked M first
-                        const int gm = min(kWGroupM, p.m_tiles - q * kWGroupM);
-                        const int r = l - q * kWGroupM * p.n_tiles;
-                        row_end = ctl->offsets[e + 1];
-                        nfo = make_int4(e, ctl->offsets[e], min(kWChunkRows, row_end - ctl->offsets[e]),
-                                        ((q * kWGroupM + r % gm) << 15) | (r / gm));
+        } else if (warp == 1) {
+            if (rank == 0) {
+                // ------------------------------------------------ MMA issuer (CTA 0 only)
+                const bool leader = elect_one();
+                StageCursor st;
+                SlotCursor cur;
+                uint32_t acc = 0, acc_phase = 0;
+                bool ok = true;
+                for (;;) {
+                    int4 info;
+                    if (!(ok = take_slot(ctl, cur, info, abort_word, p))) break;
+                    if (info.x < 0) break;
+                    if (info.z == 0) continue;
+                    const uint32_t idesc = wgrad_idesc(tile_cols(slot_n(info.w), p));
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_empty[acc]),
+                                                                          acc_phase ^ 1u, abort_word, p.timeout_ns))) {
+                        ok = false;
+                        break;
                     }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + acc * MMA_N;
+                    const int kb_n = k_blocks_of(info.z);
+                    for (int kb = 0; kb < kb_n; ++kb) {
+                        if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->full[st.stage]), st.phase,
+                                                                              abort_word, p.timeout_ns))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (leader) {
+                            const uint32_t sa = smem_u32(smem + st.stage * WSTAGE_BYTES);
+                            const uint32_t sb = sa + WHALF_BYTES;
+                            const int steps = (min(BK, info.z - kb * BK) + UMMA_K - 1) / UMMA_K;
+    #pragma unroll
+                            for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                                if (kk < steps)
+                                    mma_bf16_ss_pair(d_tmem, sw128_mnmajor_desc(sa + kk * UMMA_K * 128, WBOX_BYTES),
+                                                     sw128_mnmajor_desc(sb + kk * UMMA_K * 128, WBOX_BYTES), idesc,
+                                                     (kb | kk) != 0 ? 1u : 0u);
+                            mma_commit_pair_mc(smem_u32(&ctl->empty[st.stage]), 0x3);
+                        }
+                        __syncwarp();
+                        st.next();
+                    }
+                    if (!ok) break;
+                    if (leader) mma_commit_pair_mc(smem_u32(&ctl->tmem_full[acc]), 0x3);
+                    __syncwarp();
+                    acc ^= 1u;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
-                if (nfo.y + nfo.z >= row_end) nfo.w |= kLastChunk;
                 if (leader) {
-                    ctl->slot[cur.slot] = nfo;
-                    st_shared_cluster_v4(peer_slot0 + cur.slot * static_cast<uint32_t>(sizeof(int4)), nfo);
-                    mbar_arrive(smem_u32(&ctl->slot_full[cur.slot]));
-                    mbar_arrive_cluster(peer_slot_full0 + cur.slot * 8u);
+                    if (!ok) {
+                        raise_abort(ctl, peer);
+                        report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmMma);
+                    }
+                    // All MMAs issued complete before either CTA frees TMEM or shared memory.
+                    mma_commit_pair_mc(smem_u32(&ctl->drain), 0x1);
+                    if (!mbar_wait_bounded_cluster(smem_u32(&ctl->drain), 0u, never, p.timeout_ns))
+                        report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmDrain);
                 }
-                __syncwarp();
-                cur.next();
-                if (nfo.x < 0) break;
-            }
-        } else {
-            // ------------------------------------------------ slot-release relay (CTA 1)
-            const uint32_t slot_empty0 = mapa_shared(smem_u32(&ctl->slot_empty[0]), 0);
-            for (;;) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_empty[cur.slot]), cur.phase,
-                                                                      abort_word, p.timeout_ns))) {
-                    ok = false;
-                    break;
+            } else {
+                // ------------------------------------------------ accumulator-release relay (CTA 1)
+                // Once this CTA's epilogue warps have read an accumulator, one arrive (release at
+                // cluster scope, cumulative over theirs) frees it on CTA 0.  The epilogue warps do
+                // not arrive there themselves: a cluster-scope release waits for the stores its
+                // warp has in flight (measured 2100 to 7400 cycles of each tile).
+                const uint32_t tmem_empty0 = mapa_shared(smem_u32(&ctl->tmem_empty[0]), 0);
+                SlotCursor cur;
+                uint32_t acc = 0, acc_phase = 0;
+                bool ok = true;
+                for (;;) {
+                    int4 info;
+                    if (!(ok = take_slot(ctl, cur, info, abort_word, p))) break;
+                    if (info.x < 0) break;
+                    if (info.z == 0) continue;
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_empty[acc]), acc_phase,
+                                                                          abort_word, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_cluster(tmem_empty0 + acc * 8u);
+                    acc ^= 1u;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
-                const int e = ctl->slot[cur.slot].x;
-                __syncwarp();
-                if (leader) mbar_arrive_cluster(slot_empty0 + cur.slot * 8u);
-                cur.next();
-                if (e < 0) break;
+                if (!ok && lane == 0) {
+                    raise_abort(ctl, peer);
+                    report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmEpilogue);
+                }
             }
+            __syncwarp();
+        } else if (warp == kWSchedWarp) {
+            const bool leader = elect_one();
+            const int lead = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
+            SlotCursor cur;
+            bool ok = true;
+            if (rank == 0) {
+                // ------------------------------------------------ tile scheduler (CTA 0)
+                const uint32_t peer_slot0 = mapa_shared(smem_u32(&ctl->slot[0]), peer);
+                const uint32_t peer_slot_full0 = mapa_shared(smem_u32(&ctl->slot_full[0]), peer);
+                int4 nfo = make_int4(0, 0, 0, 0);
+                int row_end = 0;  // of the tile's expert
+                uint32_t tk = 0;
+                int batch_left = 0;
+                for (;;) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_empty[cur.slot]),
+                                                                          cur.phase ^ 1u, abort_word, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    if (nfo.y + nfo.z < row_end) {  // the tile's next chunk, in this cluster too
+                        nfo.y += nfo.z;
+                        nfo.z = min(kWChunkRows, row_end - nfo.y);
+                    } else {
+                        if (batch_left == 0) {
+                            if (leader) tk = atomicAdd(p.ticket, static_cast<uint32_t>(p.batch));
+                            tk = __shfl_sync(0xffffffffu, tk, lead);
+                            batch_left = p.batch;
+                        } else {
+                            ++tk;
+                        }
+                        --batch_left;
+                        nfo = make_int4(-1, 0, 0, 0);
+                        row_end = 0;
+                        if (tk < static_cast<uint32_t>(total_tiles)) {
+                            const int piece = tk / tiles_per_expert;
+                            const int l = tk % tiles_per_expert;
+                            const int q = l / (kWGroupM * p.n_tiles);  // group of M tiles, walked M first
+                            const int gm = min(kWGroupM, p.m_tiles - q * kWGroupM);
+                            const int r = l - q * kWGroupM * p.n_tiles;
+                            int out = 0, row = 0;
+                            if (p.split_rows != 0) {
+                                int lo = 0, hi = p.E - 1;  // largest e with index[e] <= piece
+                                while (lo < hi) {
+                                    const int mid = (lo + hi + 1) >> 1;
+                                    if (ctl->index[mid] <= piece)
+                                        lo = mid;
+                                    else
+                                        hi = mid - 1;
+                                }
+                                out = piece;
+                                row = ctl->offsets[lo] + (piece - ctl->index[lo]) * p.split_rows;
+                                row_end = min(row + p.split_rows, ctl->offsets[lo + 1]);
+                            } else {
+                                out = ctl->index[piece];
+                                row = ctl->offsets[out];
+                                row_end = ctl->offsets[out + 1];
+                            }
+                            nfo = make_int4(out, row, min(kWChunkRows, row_end - row),
+                                            ((q * kWGroupM + r % gm) << 15) | (r / gm));
+                        }
+                    }
+                    if (nfo.y + nfo.z >= row_end) nfo.w |= kLastChunk;
+                    if (leader) {
+                        ctl->slot[cur.slot] = nfo;
+                        st_shared_cluster_v4(peer_slot0 + cur.slot * static_cast<uint32_t>(sizeof(int4)), nfo);
+                        mbar_arrive(smem_u32(&ctl->slot_full[cur.slot]));
+                        mbar_arrive_cluster(peer_slot_full0 + cur.slot * 8u);
+                    }
+                    __syncwarp();
+                    cur.next(p.slots);
+                    if (nfo.x < 0) break;
+                }
+            } else {
+                // ------------------------------------------------ slot-release relay (CTA 1)
+                const uint32_t slot_empty0 = mapa_shared(smem_u32(&ctl->slot_empty[0]), 0);
+                for (;;) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->slot_empty[cur.slot]), cur.phase,
+                                                                          abort_word, p.timeout_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    const int e = ctl->slot[cur.slot].x;
+                    __syncwarp();
+                    if (leader) mbar_arrive_cluster(slot_empty0 + cur.slot * 8u);
+                    cur.next(p.slots);
+                    if (e < 0) break;
+                }
+            }
+            if (!ok && leader) {
+                raise_abort(ctl, peer);
+                report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
+            }
+            __syncwarp();
         }
-        if (!ok && leader) {
-            raise_abort(ctl, peer);
-            report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
-        }
-        __syncwarp();
     } else {
         // ---------------------------------------------------- epilogue (both CTAs, warps 4-11)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int sub = warp & 3;            // TMEM lanes [32 sub, 32 sub + 32) are this warp's
         const int half = (warp - kWEpiWarp0) >> 2;  // and columns [128 half, 128 half + 128)
-        const uint32_t tmem_empty0 = mapa_shared(smem_u32(&ctl->tmem_empty[0]), 0);
         const uint32_t buf = smem_u32(store_smem + (warp - kWEpiWarp0) * WSTORE_BYTES);
         SlotCursor cur;
+        const uint32_t buf_row = buf + lane * 128 + (lane & 7) * 16;
         uint32_t acc = 0, acc_phase = 0;
-        bool ok = true, first = true;
-        float sum[kHalfCols];
+        bool ok = true;
+        float sum[kHalfCols];  // zero between tiles
+#pragma unroll
+        for (int i = 0; i < kHalfCols; ++i) sum[i] = 0.0f;
         for (;;) {
             int4 info;
-            if (!(ok = take_slot(ctl, cur, info, abort_word, p.timeout_ns))) break;
+            if (!(ok = take_slot(ctl, cur, info, abort_word, p))) break;
             if (info.x < 0) break;
-            if (first) {
-#pragma unroll
-                for (int i = 0; i < kHalfCols; ++i) sum[i] = 0.0f;
-            }
-            if (info.z != 0) {
+            const bool rows = info.z != 0;
+            const int m_row = slot_m(info.w) * PAIR_M + static_cast<int>(rank) * BM + sub * 32;
+            const int cols = tile_cols(slot_n(info.w), p) - half * kHalfCols;  // <= 0: none for this warp
+            const int col0 = slot_n(info.w) * MMA_N + half * kHalfCols;
+            const int out_row = info.x * p.n + m_row;
+            const bool in = m_row < p.n;  // n is a multiple of 64: all 32 rows or none
+            if (rows) {
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_full[acc]), acc_phase,
                                                                       abort_word, p.timeout_ns))) {
                     ok = false;
@@ -545,56 +589,56 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                 const uint32_t tbase =
                     tmem_base + (static_cast<uint32_t>(sub * 32) << 16) + acc * MMA_N + half * kHalfCols;
 #pragma unroll
-                for (int c = 0; c < kHalfCols; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(tbase + c, v);
+                for (int c = 0; c < kHalfCols; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tbase + c, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[c + i] += __uint_as_float(v[i]);
+                    for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(v[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tmem_empty0 + acc * 8u);
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->tmem_empty[acc]));
                 acc ^= 1u;
                 if (acc == 0) acc_phase ^= 1u;
             }
-            first = (info.w & kLastChunk) != 0;
-            if (!first) continue;
-            const int m_row = slot_m(info.w) * PAIR_M + static_cast<int>(rank) * BM + sub * 32;
-            if (m_row >= p.n || (info.z == 0 && p.accumulate)) continue;  // n is a multiple of 64: all 32 rows or none
-            const int cols = tile_cols(slot_n(info.w), p) - half * kHalfCols;
-            const int col0 = slot_n(info.w) * MMA_N + half * kHalfCols;
-            const int out_row = info.x * p.n + m_row;
+            if (!(info.w & kLastChunk)) continue;
             constexpr int kCols = kBf16Out ? 64 : 32;  // columns per 128-byte row of a store
-            const uint32_t buf_row = buf + lane * 128 + (lane & 7) * 16;
+            const bool store = in && (rows || !p.accumulate);
+            const int pace = k_blocks_of(info.z) * p.pace * (kCols / 32);
+            const long long t0 = clock64();
 #pragma unroll
             for (int c = 0; c < kHalfCols; c += kCols) {
-                if (c >= cols) break;
-                if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
-                __syncwarp();
+                if (store && c < cols) {
+                    if (c != 0)
+                        while (clock64() - t0 < static_cast<long long>(c / kCols) * pace) __nanosleep(64);
+                    if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+                    __syncwarp();
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    uint4 o;
-                    if (kBf16Out)
-                        o = make_uint4(pack_bf16x2(sum[c + 8 * q], sum[c + 8 * q + 1]),
-                                       pack_bf16x2(sum[c + 8 * q + 2], sum[c + 8 * q + 3]),
-                                       pack_bf16x2(sum[c + 8 * q + 4], sum[c + 8 * q + 5]),
-                                       pack_bf16x2(sum[c + 8 * q + 6], sum[c + 8 * q + 7]));
-                    else
-                        o = make_uint4(__float_as_uint(sum[c + 4 * q]), __float_as_uint(sum[c + 4 * q + 1]),
-                                       __float_as_uint(sum[c + 4 * q + 2]), __float_as_uint(sum[c + 4 * q + 3]));
-                    st_shared_v4(buf_row ^ (q * 16), o);
+                    for (int q = 0; q < 8; ++q) {
+                        uint4 o;
+                        if (kBf16Out)
+                            o = make_uint4(pack_bf16x2(sum[c + 8 * q], sum[c + 8 * q + 1]),
+                                           pack_bf16x2(sum[c + 8 * q + 2], sum[c + 8 * q + 3]),
+                                           pack_bf16x2(sum[c + 8 * q + 4], sum[c + 8 * q + 5]),
+                                           pack_bf16x2(sum[c + 8 * q + 6], sum[c + 8 * q + 7]));
+                        else
+                            o = make_uint4(__float_as_uint(sum[c + 4 * q]), __float_as_uint(sum[c + 4 * q + 1]),
+                                           __float_as_uint(sum[c + 4 * q + 2]), __float_as_uint(sum[c + 4 * q + 3]));
+                        st_shared_v4(buf_row ^ (q * 16), o);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (!kBf16Out && p.accumulate)
+                            tma_reduce_add_2d(&tmOut, col0 + c, out_row, buf);
+                        else
+                            tma_store_2d(&tmOut, col0 + c, out_row, buf);
+                        bulk_commit();
+                    }
                 }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    if (!kBf16Out && p.accumulate)
-                        tma_reduce_add_2d(&tmOut, col0 + c, out_row, buf);
-                    else
-                        tma_store_2d(&tmOut, col0 + c, out_row, buf);
-                    bulk_commit();
-                }
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) sum[c + i] = 0.0f;
             }
         }
         if (lane == 0) {
@@ -639,8 +683,68 @@ bool make_map_box(CUtensorMap* m, const void* base, bool fp32, uint64_t inner, u
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Adds an expert's pieces, part [pieces, n, d] fp32, in row order into dw (+=
+// with `accumulate`): a block per 1024 values of one expert.
 template <bool kBf16Out>
-cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const WgradParams& p,
+__global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict__ part,
+                                                         const int32_t* __restrict__ offsets, int split_rows,
+                                                         int64_t size, void* dw, int accumulate,
+                                                         const uint32_t* __restrict__ status) {
+    __shared__ int first;
+    if (*status != 0u) return;  // rejected offsets, or a wait that ran out: dw stays as it is
+    const int e = blockIdx.y;
+    if (threadIdx.x == 0) first = 0;
+    __syncthreads();
+    int before = 0;
+    for (int q = threadIdx.x; q < e; q += 256) before += pieces_of(offsets[q + 1] - offsets[q], split_rows);
+    if (before != 0) atomicAdd(&first, before);
+    __syncthreads();
+    const int n = pieces_of(offsets[e + 1] - offsets[e], split_rows);
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= size) return;
+    const float* src = part + static_cast<int64_t>(first) * size + i;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int q = 0; q < n; ++q) {
+        const float4 t = __ldcs(reinterpret_cast<const float4*>(src + q * size));
+        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+    }
+    if (kBf16Out) {
+        *reinterpret_cast<uint2*>(static_cast<bf16*>(dw) + e * size + i) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    } else {
+        float4* out = reinterpret_cast<float4*>(static_cast<float*>(dw) + e * size + i);
+        if (accumulate) {
+            const float4 t = *out;
+            v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+        }
+        *out = v;
+    }
+}
+
+// Rows of a piece, or 0 where the experts are summed whole.  Pieces make about
+// two tiles per cluster and have at least 512 rows.  They pay where the tiles
+// are too few: whole sums take the k-blocks of an expert (half as many again
+// for uneven ones) per wave of tiles, at 512 cycles (0.27 us) each; pieces share
+// the k-blocks out, but are stored and read back (about 8 TB/s through L2) and
+// cost a second kernel.  Measured, fp32: 30000 rows of 4 experts of 256 x 256:
+// whole 43 us, in pieces 23; 131072 rows of one 64 x 64: 535 and 35; 20000 rows
+// of 8 experts of 1024 x 512 (64 tiles): 34 and 44.
+int split_rows_of(int64_t S, int d, int E, int n) {
+    const int64_t per_expert = static_cast<int64_t>((n + PAIR_M - 1) / PAIR_M) * ((d + MMA_N - 1) / MMA_N);
+    if (per_expert * E >= 2 * kClusters) return 0;
+    const int64_t rows = std::max<int64_t>(512, (S * per_expert / (2 * kClusters) + BK - 1) / BK * BK);
+    if (rows >= S) return 0;
+    const double block_us = 0.27;
+    const double waves = static_cast<double>((per_expert * E + kClusters - 1) / kClusters);
+    const double whole = 1.5 * waves * S / E / BK * block_us;
+    const double shared = static_cast<double>(S) * per_expert / BK / kClusters * block_us;
+    const double join = 2.0 * (S / rows + E) * n * d * sizeof(float) / 8e6 + 5.0;
+    return shared + join < whole ? static_cast<int>(rows) : 0;
+}
+
+template <bool kBf16Out>
+cudaError_t launch_wgrad(const OperandMaps& a, const OperandMaps& b, const CUtensorMap& out, const WgradParams& p,
                          cudaStream_t s) {
     static std::atomic<int> max_clusters[64];  // per device, 0 until configured
     int dev = 0;
@@ -657,7 +761,8 @@ cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUten
         if (n < 1) return cudaErrorInvalidConfiguration;
         if (dev < 64) max_clusters[dev].store(n, std::memory_order_release);
     }
-    const int64_t tiles = static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles;
+    // with pieces: an upper bound (every expert adds at most one partial piece)
+    const int64_t tiles = (p.split_rows != 0 ? p.S / p.split_rows + p.E : p.E) * static_cast<int64_t>(p.m_tiles) * p.n_tiles;
     lc.cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(n, tiles)));
     err = cudaLaunchKernelEx(&lc.cfg, fn, a, b, out, p);
     if (err != cudaSuccess) return err;
@@ -668,6 +773,12 @@ cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUten
 }  // namespace mk
 
 using namespace mk;
+
+extern "C" size_t mk_moe_grouped_wgrad_workspace_size(int64_t S, int d, int E, int n) {
+    if (check_sizes(S, d, E, 1, n) != MK_OK) return 0;
+    const int rows = split_rows_of(S, d, E, n);
+    return 256 + (rows == 0 ? 0 : static_cast<size_t>(S / rows + E) * n * d * sizeof(float));
+}
 
 extern "C" mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* expert_offsets, const void* x_perm,
                                           int64_t S, int d, int E, int n, void* dw, int dw_type, int accumulate,
@@ -693,9 +804,18 @@ extern "C" mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* exper
             return MK_ERR_CUDA;
         return MK_OK;
     }
-    CUtensorMap a, b, out;
-    if (!make_map_box(&a, dout, false, n, S, BK) || !make_map_box(&b, x_perm, false, d, S, BK) ||
-        !make_map_box(&out, dw, fp32, d, static_cast<uint64_t>(E) * n, 32))
+    OperandMaps a, b;
+    // Pieces need room for their sums; a caller with the least workspace gets whole experts.
+    const int split =
+        ws_bytes >= mk_moe_grouped_wgrad_workspace_size(S, d, E, n) ? split_rows_of(S, d, E, n) : 0;
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+    const bool sums = fp32 || split != 0;  // the tiles' type
+    CUtensorMap out;
+    for (int i = 0; i < kBoxes; ++i)
+        if (!make_map_box(&a.m[i], dout, false, n, S, BK >> i) || !make_map_box(&b.m[i], x_perm, false, d, S, BK >> i))
+            return MK_ERR_CUDA;
+    if (!make_map_box(&out, split != 0 ? part : dw, sums, d,
+                      static_cast<uint64_t>(split != 0 ? S / split + E : E) * n, 32))
         return MK_ERR_CUDA;
     WgradParams p;
     p.offsets = expert_offsets;
@@ -705,10 +825,29 @@ extern "C" mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* exper
     p.d = d;
     p.m_tiles = static_cast<int>(m_tiles);
     p.n_tiles = static_cast<int>(n_tiles);
-    p.accumulate = accumulate ? 1 : 0;
+    p.accumulate = accumulate && split == 0 ? 1 : 0;
+    p.split_rows = split;
+    // A ticket takes about 1 us, a tile of an expert with few rows little more: then tiles are
+    // claimed four at a time and eight ahead.  Otherwise three ahead, so that a cluster holds few
+    // at the end.  Measured, 256 experts of 1408 x 2048 bf16 with 32 rows: 332 us, one at a time
+    // 385; 32 experts of 512 rows: eight ahead 125 us, three 108.
+    const bool short_tiles = S <= 128 * static_cast<int64_t>(E);
+    const int64_t tiles = m_tiles * n_tiles * E;
+    p.slots = short_tiles ? kWSlots : 3;
+    p.batch = short_tiles && tiles >= 64 * kClusters ? 4 : 1;
+    p.pace = tiles >= 8 * kClusters ? kStorePace : 0;
     p.status = status;
     p.ticket = status + 4;
     p.timeout_ns = kDefaultTimeoutNs;
-    const cudaError_t err = fp32 ? launch_wgrad<false>(a, b, out, p, s) : launch_wgrad<true>(a, b, out, p, s);
+    cudaError_t err = sums ? launch_wgrad<false>(a, b, out, p, s) : launch_wgrad<true>(a, b, out, p, s);
+    if (err == cudaSuccess && split != 0) {
+        const int64_t size = static_cast<int64_t>(n) * d;
+        const dim3 grid(static_cast<unsigned>((size + 1023) / 1024), static_cast<unsigned>(E));
+        if (fp32)
+            wgrad_join_kernel<false><<<grid, 256, 0, s>>>(part, expert_offsets, split, size, dw, accumulate, status);
+        else
+            wgrad_join_kernel<true><<<grid, 256, 0, s>>>(part, expert_offsets, split, size, dw, 0, status);
+        err = cudaGetLastError();
+    }
     return err == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

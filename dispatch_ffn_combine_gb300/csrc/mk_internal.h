@@ -33,7 +33,6 @@ enum : uint32_t {
     kSiteRegroup = 0xA00,
     kSiteCkptSlot = 0xB00,
     kSiteWgradOffsets = 0xC00,
-    kSiteWgradTail = 0xD00,
 };
 
 // Byte offsets of every region of the caller's workspace.  The first 256

@@ -444,9 +444,12 @@ MK_API mk_status mk_moe_grouped_dgrad(const void* dout, const int32_t* expert_of
  *   dw   [E, n, d] (out): dw_type MK_TYPE_FP32 or MK_TYPE_BF16.  accumulate != 0
  *        (fp32 only) adds to dw; otherwise dw is overwritten, with zeros for an
  *        expert without rows (and for all of them when S == 0).
- *   ws: at least 256 bytes.
+ *   ws: at least 256 bytes.  With mk_moe_grouped_wgrad_workspace_size() bytes
+ *        the sums of few, long experts are split over the GPU and joined in row
+ *        order (the same sums, rounded in another order).
  * Rows of one expert never reach another's gradient, NaN and infinities
  * included.  Bad offsets set MK_ERR_BOUNDS on the device and dw is untouched. */
+MK_API size_t mk_moe_grouped_wgrad_workspace_size(int64_t S, int d, int E, int n);
 MK_API mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* expert_offsets, const void* x_perm,
                                int64_t S, int d, int E, int n, void* dw, int dw_type, int accumulate,
                                void* ws, size_t ws_bytes, void* stream);

@@ -152,6 +152,36 @@ def test_wgrad_long_sum_keeps_fp32_accuracy():
     assert float((dw - want).norm() / want.norm()) <= 2e-6
 
 
+@pytest.mark.parametrize("counts,n,d", [([20000], 64, 64), ([9000, 0, 3001, 1], 256, 192), ([511, 13000], 64, 256)])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.float32, False), (torch.float32, True), (BF, False)])
+def test_wgrad_few_long_experts_in_pieces(counts, n, d, dtype, accumulate):
+    """Few tiles and long sums: with the workspace of its size function the sum is cut into pieces and
+    joined (ragged pieces, experts without any), without it it is not; both within the bounds."""
+    S, E = sum(counts), len(counts)
+    off = _offsets(counts)
+    do, x = _randn((S, n), 1), _randn((S, d), 2)
+    size = mk.load_library().mk_moe_grouped_wgrad_workspace_size(S, d, E, n)
+    assert size > 256 + 2 * n * d * 4
+    before = _randn((E, n, d), 3, dtype=dtype)
+    want = ref.wgrad(do, off, x, E) + (before.to(F64) if accumulate else 0)
+    slack = max(counts) * 2.0 ** -23 * (ref.wgrad(do.abs(), off, x.abs(), E) + before.to(F64).abs())
+    for nbytes in (size, 256):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+        dw = before.clone()
+        mk.mk_moe_grouped_wgrad(do, off, x, dw=dw, accumulate=accumulate, ws=ws)
+        assert mk.mk_moe_last_device_error(ws)[0] == mk.MK_OK
+        _close(dw, want, slack, "bf16 dw" if dtype == BF else "fp32 dw")
+        again = before.clone()
+        mk.mk_moe_grouped_wgrad(do, off, x, dw=again, accumulate=accumulate, ws=ws)
+        assert torch.equal(dw, again)
+    bad = off.clone()
+    bad[1] = S + 5
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    dw = before.clone()
+    mk.mk_moe_grouped_wgrad(do, bad, x, dw=dw, accumulate=accumulate, ws=ws)
+    assert mk.mk_moe_last_device_error(ws)[0] == mk.MK_ERR_BOUNDS and torch.equal(dw, before)
+
+
 def test_wgrad_without_rows():
     off = torch.zeros(3, dtype=torch.int32, device=DEV)
     do, x = torch.empty((0, 64), dtype=BF, device=DEV), torch.empty((0, 128), dtype=BF, device=DEV)
