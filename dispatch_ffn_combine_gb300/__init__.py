@@ -562,7 +562,7 @@ def _new(t, dtype, shape, like, stream):
     again before that stream is done with it."""
     if t is not None:
         return t
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+    t = torch.empty(*shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream)
     return t

@@ -347,8 +347,7 @@ mk_status mk_moe_grouped_dgrad(const void* dout, const int32_t* expert_offsets, 
     a.dx = static_cast<bf16*>(dx);
     a.status = at<uint32_t>(ws, 0);
     a.ticket = a.status + 4;
-    MK_TRY(cudaMemsetAsync(a.status, 0, 32, s));  // status, site, tile ticket
-    MK_TRY(launch_mtile_table(expert_offsets, E, S, at<int32_t>(ws, 256), a.status, s));
+    MK_TRY(launch_mtile_table(expert_offsets, E, S, at<int32_t>(ws, 256), a.status, s, true));
     MK_TRY(launch_grouped_dgrad(a, s));
     return MK_OK;
 }

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kThreads) ckpt8_dispatch_kernel(const uint8_t*
                                                                   uint32_t* status) {
     __shared__ int64_t rows[kMaxTopK];
     const int64_t t = blockIdx.x;
+    pdl_wait();  // the status comes from the kernel before
     if (threadIdx.x < k) {
         const int64_t r = slot_row[t * k + threadIdx.x];
         const bool ok = r >= 0 && r < S;
@@ -229,10 +230,11 @@ extern "C" mk_status mk_moe_ckpt8_dispatch(const uint8_t* codes, const uint8_t* 
     if (!device_is_sm103()) return MK_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint32_t* status = static_cast<uint32_t*>(ws);
-    if (cudaMemsetAsync(status, 0, 8, s) != cudaSuccess) return MK_ERR_CUDA;
-    ckpt8_dispatch_kernel<<<static_cast<unsigned>(T), kThreads, 0, s>>>(codes, scales, slot_row, T * k, d, k,
-                                                                         static_cast<bf16*>(x_perm), status);
-    return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    if (launch_clear_control(status, s) != cudaSuccess) return MK_ERR_CUDA;
+    LaunchCfg lc(dim3(static_cast<unsigned>(T)), dim3(kThreads), 0, s, true);
+    const cudaError_t err = cudaLaunchKernelEx(&lc.cfg, ckpt8_dispatch_kernel, codes, scales, slot_row, T * k, d, k,
+                                               static_cast<bf16*>(x_perm), status);
+    return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
 extern "C" mk_status mk_moe_swiglu_ckpt8(const void* gate, const void* up, int64_t S, int f, void* h, uint8_t* codes,

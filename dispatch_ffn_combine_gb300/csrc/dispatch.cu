@@ -161,12 +161,16 @@ __global__ void __launch_bounds__(1024) scan_kernel(const int32_t* __restrict__ 
 
 // Tile table for caller-supplied offsets (expert FFN entry point).  Offsets
 // that are not a non-decreasing sequence from 0 to S are rejected: the error
-// is recorded and the table is zeroed so the GEMMs run no tiles.
+// is recorded and the table is zeroed so the GEMMs run no tiles.  `clear`: the
+// control words (status, site, tickets) are zeroed here first.
 __global__ void __launch_bounds__(32) mtile_table_kernel(const int32_t* __restrict__ offsets, int E, int64_t S,
-                                                         int32_t* __restrict__ mtile_start, uint32_t* status) {
+                                                         int32_t* __restrict__ mtile_start, uint32_t* status,
+                                                         int clear) {
     __shared__ int32_t s_counts[kMaxExperts];
     __shared__ int bad;
     const int lane = threadIdx.x;
+    pdl_launch_dependents();
+    if (clear && lane < kControlWords) status[lane] = 0u;
     if (lane == 0) bad = (offsets[0] != 0 || offsets[E] != S) ? 1 : 0;
     __syncwarp();
     for (int e = lane; e < E; e += 32) {
@@ -279,8 +283,20 @@ cudaError_t launch_scan(const int32_t* chunk_counts, int64_t nchunks, int E, int
 }
 
 cudaError_t launch_mtile_table(const int32_t* offsets, int E, int64_t S, int32_t* mtile_start, uint32_t* status,
-                               cudaStream_t s) {
-    mtile_table_kernel<<<1, 32, 0, s>>>(offsets, E, S, mtile_start, status);
+                               cudaStream_t s, bool clear) {
+    mtile_table_kernel<<<1, 32, 0, s>>>(offsets, E, S, mtile_start, status, clear ? 1 : 0);
+    return cudaGetLastError();
+}
+
+// The control words alone, for kernels that need no table; the kernel after it
+// may be launched as its programmatic dependent.
+__global__ void __launch_bounds__(32) clear_control_kernel(uint32_t* status) {
+    pdl_launch_dependents();
+    if (threadIdx.x < kControlWords) status[threadIdx.x] = 0u;
+}
+
+cudaError_t launch_clear_control(uint32_t* status, cudaStream_t s) {
+    clear_control_kernel<<<1, 32, 0, s>>>(status);
     return cudaGetLastError();
 }
 

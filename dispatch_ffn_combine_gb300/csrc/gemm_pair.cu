@@ -226,6 +226,8 @@ __global__ void __launch_bounds__(PNUM_THREADS, 1)
     const uint32_t rank = cluster_ctarank();
     const uint32_t peer = rank ^ 1u;
 
+    if (MODE == 2) pdl_wait();  // the table, the ticket and the status come from the kernel before
+
     // Tile table in shared memory: the pair-block prefix (an expert with t
     // 128-row blocks has ceil(t / 2) pair blocks).
     if (warp == 0) {
@@ -743,7 +745,7 @@ cudaError_t launch_pair_mode(const PairMaps& m, const ActMaps& m2, const PairPar
     const int64_t resident = max_clusters[slot].load(std::memory_order_relaxed);
     const int clusters = static_cast<int>(std::min<int64_t>(resident, std::max<int64_t>(max_tiles, 1)));
     cfg.gridDim = dim3(2 * clusters);
-    LaunchCfg lc(cfg.gridDim, cfg.blockDim, PSMEM_BYTES, s, p.pdl != 0, 2);
+    LaunchCfg lc(cfg.gridDim, cfg.blockDim, PSMEM_BYTES, s, p.pdl != 0 || MODE == 2, 2);
     err = cudaLaunchKernelEx(&lc.cfg, fn, m.a, m.b0, m.b1, m.a16, m.a32, m.a64, m.b0q, m.b1q, m2, p);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();

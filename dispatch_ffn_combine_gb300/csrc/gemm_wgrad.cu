@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
         ctl->index[my_e] = static_cast<uint16_t>(min(before, 0xffff));  // few: fewer tiles than clusters are split
     }
     if (my_e == 0) bad = bad || ctl->offsets[0] != 0 || ctl->offsets[p.E] != p.S;
+    pdl_wait();  // the control words come from the kernel before
     const bool rejected = __syncthreads_or(bad ? 1 : 0) != 0;
     if (rejected && blockIdx.x == 0 && threadIdx.x == 0) report_error(p.status, MK_ERR_BOUNDS, kSiteWgradOffsets);
     tc_fence_before();
@@ -751,7 +752,7 @@ cudaError_t launch_wgrad(const OperandMaps& a, const OperandMaps& b, const CUten
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     auto fn = grouped_wgrad_kernel<kBf16Out>;
-    LaunchCfg lc(dim3(2 * std::max(1, device_sm_count() / 2)), dim3(WNUM_THREADS), WSMEM_BYTES, s, false, 2);
+    LaunchCfg lc(dim3(2 * std::max(1, device_sm_count() / 2)), dim3(WNUM_THREADS), WSMEM_BYTES, s, true, 2);
     int n = dev < 64 ? max_clusters[dev].load(std::memory_order_acquire) : 0;
     if (n == 0) {
         err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(WSMEM_BYTES));
@@ -796,7 +797,7 @@ extern "C" mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* exper
     if (!device_is_sm103()) return MK_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint32_t* status = static_cast<uint32_t*>(ws);
-    if (cudaMemsetAsync(status, 0, 32, s) != cudaSuccess) return MK_ERR_CUDA;  // status, site, tile ticket
+    if (launch_clear_control(status, s) != cudaSuccess) return MK_ERR_CUDA;
     const bool fp32 = dw_type == MK_TYPE_FP32;
     if (S == 0) {  // no rows: every expert's gradient is zero
         if (!accumulate &&

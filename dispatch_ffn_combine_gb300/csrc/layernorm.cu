@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
                 p.store(v, dx + at + kLaneStep * v, c);
             }
     }
+    pdl_launch_dependents();  // the kernel that adds the partial rows
     // The block's partial row [dgamma d | dbeta d]: every group's sums side by
     // side in shared memory, added in group order.
     float* sums = reinterpret_cast<float*>(ring);
@@ -445,6 +446,7 @@ __global__ void __launch_bounds__(256) layernorm_bwd_sum_kernel(const float* __r
                                                                 float* __restrict__ dgamma,
                                                                 float* __restrict__ dbeta) {
     __shared__ float s[8][32];
+    pdl_wait();  // the partial rows come from the kernel before
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float v = 0.0f;
@@ -656,7 +658,9 @@ extern "C" mk_status mk_moe_layernorm_bwd(const void* dy, const void* x, int x_t
     a.dy = dy, a.dres = dres, a.dx = dx;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
     if ((x_type == MK_TYPE_FP32 ? run_bwd<float>(a) : run_bwd<bf16>(a)) != cudaSuccess) return MK_ERR_CUDA;
-    layernorm_bwd_sum_kernel<<<static_cast<unsigned>((2 * static_cast<int64_t>(d) + 31) / 32), 256, 0, s>>>(
-        a.part, a.blocks, d, dgamma, dbeta);
+    const LaunchCfg lc(dim3(static_cast<unsigned>((2 * static_cast<int64_t>(d) + 31) / 32)), dim3(256), 0, s, true);
+    if (cudaLaunchKernelEx(&lc.cfg, layernorm_bwd_sum_kernel, static_cast<const float*>(a.part), a.blocks, d, dgamma,
+                           dbeta) != cudaSuccess)
+        return MK_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

@@ -156,8 +156,11 @@ cudaError_t launch_scatter(const bf16* x, const int32_t* ids, const float* w, in
                            int32_t* row_token, float* row_weight, int32_t* slot_row, cudaStream_t s,
                            const TileSems* sem = nullptr, const int32_t* mtile_start = nullptr,
                            bool copy_rows = true);
+// `clear`: the control words are zeroed first (else by the caller).
+constexpr int kControlWords = 8;  // at the start of a workspace: status, site, -, -, tickets
 cudaError_t launch_mtile_table(const int32_t* offsets, int E, int64_t S, int32_t* mtile_start, uint32_t* status,
-                               cudaStream_t s);
+                               cudaStream_t s, bool clear = false);
+cudaError_t launch_clear_control(uint32_t* status, cudaStream_t s);
 // y[t] = sum_j P[slot_row[t, j]] for t < T; p_rows = rows of P (-1: T * k).
 // Copy `bytes` (a multiple of 16; both pointers 16-byte aligned) between
 // device memory and mapped page-locked host memory with `blocks` CTAs of plain
