@@ -140,6 +140,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int32_t c0,
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {  // into L2
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t src) {
     asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -579,6 +586,11 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
             const int col0 = slot_n(info.w) * MMA_N + half * kHalfCols;
             const int out_row = info.x * p.n + m_row;
             const bool in = m_row < p.n;  // n is a multiple of 64: all 32 rows or none
+            constexpr int kCols = kBf16Out ? 64 : 32;  // columns per 128-byte row of a store
+            const bool last = (info.w & kLastChunk) != 0;
+            const bool store = in && (rows || !p.accumulate);
+            if (!kBf16Out && p.accumulate && last && store && lane == 0)
+                for (int c = 0; c < kHalfCols && c < cols; c += kCols) tma_prefetch_2d(&tmOut, col0 + c, out_row);
             if (rows) {
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_full[acc]), acc_phase,
                                                                       abort_word, p.timeout_ns))) {
@@ -603,9 +615,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                 acc ^= 1u;
                 if (acc == 0) acc_phase ^= 1u;
             }
-            if (!(info.w & kLastChunk)) continue;
-            constexpr int kCols = kBf16Out ? 64 : 32;  // columns per 128-byte row of a store
-            const bool store = in && (rows || !p.accumulate);
+            if (!last) continue;
             const int pace = k_blocks_of(info.z) * p.pace * (kCols / 32);
             const long long t0 = clock64();
 #pragma unroll
