@@ -55,13 +55,17 @@ namespace {
 
 using namespace gemm_detail;
 
-constexpr int WSTAGES = 6;
+// Stages of the operand ring and store buffers per epilogue warp, which share
+// the 224 KB beside the control block: tiles with long sums take a sixth stage,
+// short ones (bound by their stores) a second buffer.
+constexpr int kLongStages = 6, kLongBufs = 1;
+constexpr int kShortStages = 5, kShortBufs = 2;
+constexpr int kMaxStages = 6;
 constexpr uint32_t WBOX_BYTES = 64 * BK * 2;             // 64 columns of 64 rows
 constexpr uint32_t WHALF_BYTES = 2 * WBOX_BYTES;         // 128 columns
 constexpr uint32_t WSTAGE_BYTES = 2 * WHALF_BYTES;       // this CTA's dout and x columns
 constexpr int kWEpiWarps = 8;                            // two per TMEM quarter, half of the columns each
 constexpr uint32_t WSTORE_BYTES = 32 * 128;              // one store of an epilogue warp
-constexpr uint32_t WSTORE_ALL = kWEpiWarps * WSTORE_BYTES;
 constexpr int kWSchedWarp = 2;
 constexpr int kWEpiWarp0 = 4;  // registers move between warpgroups; warp 3 only fills up the first
 constexpr int WNUM_THREADS = 32 * (kWEpiWarp0 + kWEpiWarps);
@@ -85,8 +89,8 @@ constexpr int kClusters = 76;  // what the splitting and pacing rules assume res
 constexpr int kWGroupM = 8;  // M tiles walked together: tiles claimed together share operand columns in L2
 
 struct WgradCtl {
-    uint64_t full[WSTAGES];   // CTA 0: both CTAs' copies of the stage landed
-    uint64_t empty[WSTAGES];  // each CTA: the MMAs that read the stage are done
+    uint64_t full[kMaxStages];   // CTA 0: both CTAs' copies of the stage landed
+    uint64_t empty[kMaxStages];  // each CTA: the MMAs that read the stage are done
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];  // each CTA: its epilogue warps have read the accumulator (CTA 0: and CTA 1's)
     // the accumulator
@@ -102,8 +106,12 @@ struct WgradCtl {
 };
 
 static_assert(WNUM_THREADS > kMaxExperts, "the prologue has a thread per offset");
-constexpr size_t WSMEM_BYTES = static_cast<size_t>(WSTAGES) * WSTAGE_BYTES + WSTORE_ALL + sizeof(WgradCtl) + 1024;
-static_assert(WSMEM_BYTES <= 227u * 1024u, "weight-gradient shared memory exceeds the per-CTA limit");
+constexpr size_t wgrad_smem(int stages, int bufs) {
+    return static_cast<size_t>(stages) * WSTAGE_BYTES + static_cast<size_t>(kWEpiWarps * bufs) * WSTORE_BYTES +
+           sizeof(WgradCtl) + 1024;
+}
+static_assert(wgrad_smem(kLongStages, kLongBufs) <= 227u * 1024u && wgrad_smem(kShortStages, kShortBufs) <= 227u * 1024u,
+              "weight-gradient shared memory exceeds the per-CTA limit");
 
 // One operand [S, columns] in boxes of 64 columns x 64, 32, 16, 8, 4, 2 and 1 rows.
 constexpr int kBoxes = 7;
@@ -195,10 +203,11 @@ __device__ __forceinline__ bool take_slot(WgradCtl* ctl, SlotCursor& cur, int4& 
     return true;
 }
 
+template <int kStages>
 struct StageCursor {
     uint32_t stage = 0, phase = 0;
     __device__ __forceinline__ void next() {
-        if (++stage == WSTAGES) {
+        if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -221,14 +230,14 @@ __device__ __forceinline__ int tile_cols(int n_tile, const WgradParams& p) {
 
 constexpr int kHalfCols = MMA_N / 2;
 
-template <bool kBf16Out>
+template <bool kBf16Out, int kStages, int kBufs>
 __global__ void __launch_bounds__(WNUM_THREADS, 1)
     grouped_wgrad_kernel(const __grid_constant__ OperandMaps tmA, const __grid_constant__ OperandMaps tmB,
                          const __grid_constant__ CUtensorMap tmOut, const WgradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* store_smem = smem + WSTAGES * WSTAGE_BYTES;
-    WgradCtl* ctl = reinterpret_cast<WgradCtl*>(store_smem + WSTORE_ALL);
+    uint8_t* store_smem = smem + kStages * WSTAGE_BYTES;
+    WgradCtl* ctl = reinterpret_cast<WgradCtl*>(store_smem + kWEpiWarps * kBufs * WSTORE_BYTES);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
     const int my_e = threadIdx.x;
     if (my_e <= p.E) ctl->offsets[my_e] = p.offsets[my_e];
     if (threadIdx.x == 0) {
-        for (int s = 0; s < WSTAGES; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
@@ -296,15 +305,15 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
     const int tiles_per_expert = p.m_tiles * p.n_tiles;
     const int total_tiles = rejected ? 0 : (p.split_rows != 0 ? ctl->index[p.E] : p.E) * tiles_per_expert;
 
-    // The epilogue warps take the registers (their sums) that the other four give up: 64 + 2 x 216 of the
+    // The epilogue warps take the registers (their sums) that the other four give up: 40 + 2 x 232 of the
     // 3 x 168 per warp that the block is launched with.
     if (warp < kWEpiWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             // ---------------------------------------------------- TMA producer (both CTAs)
             const bool leader = elect_one();
             const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
-            StageCursor st;
+            StageCursor<kStages> st;
             SlotCursor cur;
             uint32_t issued = 0, last_par = 0;
             bool ok = true;
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                     report_error(p.status, MK_ERR_TIMEOUT, kSiteGemmProducer);
                 }
                 // CTA 0: every stage it armed completes (or times out) before the CTA exits
-                for (int s = 0; s < WSTAGES; ++s)
+                for (int s = 0; s < kStages; ++s)
                     if ((issued >> s) & 1u)
                         mbar_wait_bounded_cluster(smem_u32(&ctl->full[s]), (last_par >> s) & 1u, never, p.timeout_ns);
             }
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
             if (rank == 0) {
                 // ------------------------------------------------ MMA issuer (CTA 0 only)
                 const bool leader = elect_one();
-                StageCursor st;
+                StageCursor<kStages> st;
                 SlotCursor cur;
                 uint32_t acc = 0, acc_phase = 0;
                 bool ok = true;
@@ -565,12 +574,12 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
         }
     } else {
         // ---------------------------------------------------- epilogue (both CTAs, warps 4-11)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int sub = warp & 3;            // TMEM lanes [32 sub, 32 sub + 32) are this warp's
         const int half = (warp - kWEpiWarp0) >> 2;  // and columns [128 half, 128 half + 128)
-        const uint32_t buf = smem_u32(store_smem + (warp - kWEpiWarp0) * WSTORE_BYTES);
+        uint32_t buf = smem_u32(store_smem + (warp - kWEpiWarp0) * (kBufs * WSTORE_BYTES));
         SlotCursor cur;
-        const uint32_t buf_row = buf + lane * 128 + (lane & 7) * 16;
+        const uint32_t buf_row = lane * 128 + (lane & 7) * 16;
         uint32_t acc = 0, acc_phase = 0;
         bool ok = true;
         float sum[kHalfCols];  // zero between tiles
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                 if (store && c < cols) {
                     if (c != 0)
                         while (clock64() - t0 < static_cast<long long>(c / kCols) * pace) __nanosleep(64);
-                    if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+                    if (lane == 0) bulk_wait_read<kBufs - 1>();  // the last store from this buffer has read it
                     __syncwarp();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -636,7 +645,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                         else
                             o = make_uint4(__float_as_uint(sum[c + 4 * q]), __float_as_uint(sum[c + 4 * q + 1]),
                                            __float_as_uint(sum[c + 4 * q + 2]), __float_as_uint(sum[c + 4 * q + 3]));
-                        st_shared_v4(buf_row ^ (q * 16), o);
+                        st_shared_v4(buf + (buf_row ^ (q * 16)), o);
                     }
                     fence_proxy_async_shared();
                     __syncwarp();
@@ -647,6 +656,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                             tma_store_2d(&tmOut, col0 + c, out_row, buf);
                         bulk_commit();
                     }
+                    if (kBufs == 2) buf ^= WSTORE_BYTES;  // the pair is aligned to its size
                 }
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) sum[c + i] = 0.0f;
@@ -754,18 +764,19 @@ int split_rows_of(int64_t S, int d, int E, int n) {
     return shared + join < whole ? static_cast<int>(rows) : 0;
 }
 
-template <bool kBf16Out>
+template <bool kBf16Out, int kStages, int kBufs>
 cudaError_t launch_wgrad(const OperandMaps& a, const OperandMaps& b, const CUtensorMap& out, const WgradParams& p,
                          cudaStream_t s) {
     static std::atomic<int> max_clusters[64];  // per device, 0 until configured
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    auto fn = grouped_wgrad_kernel<kBf16Out>;
-    LaunchCfg lc(dim3(2 * std::max(1, device_sm_count() / 2)), dim3(WNUM_THREADS), WSMEM_BYTES, s, true, 2);
+    auto fn = grouped_wgrad_kernel<kBf16Out, kStages, kBufs>;
+    constexpr size_t smem = wgrad_smem(kStages, kBufs);
+    LaunchCfg lc(dim3(2 * std::max(1, device_sm_count() / 2)), dim3(WNUM_THREADS), smem, s, true, 2);
     int n = dev < 64 ? max_clusters[dev].load(std::memory_order_acquire) : 0;
     if (n == 0) {
-        err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(WSMEM_BYTES));
+        err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (err != cudaSuccess) return err;
         err = cudaOccupancyMaxActiveClusters(&n, fn, &lc.cfg);
         if (err != cudaSuccess) return err;
@@ -850,7 +861,11 @@ extern "C" mk_status mk_moe_grouped_wgrad(const void* dout, const int32_t* exper
     p.status = status;
     p.ticket = status + 4;
     p.timeout_ns = kDefaultTimeoutNs;
-    cudaError_t err = sums ? launch_wgrad<false>(a, b, out, p, s) : launch_wgrad<true>(a, b, out, p, s);
+    auto run = sums ? (short_tiles ? launch_wgrad<false, kShortStages, kShortBufs>
+                                   : launch_wgrad<false, kLongStages, kLongBufs>)
+                    : (short_tiles ? launch_wgrad<true, kShortStages, kShortBufs>
+                                   : launch_wgrad<true, kLongStages, kLongBufs>);
+    cudaError_t err = run(a, b, out, p, s);
     if (err == cudaSuccess && split != 0) {
         const int64_t size = static_cast<int64_t>(n) * d;
         const dim3 grid(static_cast<unsigned>((size + 1023) / 1024), static_cast<unsigned>(E));
