@@ -27,7 +27,7 @@ __device__ __forceinline__ void topk_token(const float* __restrict__ logits, int
 #pragma unroll
     for (int q = 0; q < kMaxExperts / 32; ++q) {
         const int e = lane + 32 * q;
-        v[q] = (e < E) ? logits[t * E + e] : 0.0f;
+        v[q] = (e < E) ? rankable(logits[t * E + e]) : 0.0f;
     }
     uint32_t taken = 0;
     float sel_v[kMaxTopK];

@@ -51,7 +51,8 @@ cudaError_t launch_logits_shape(const uint16_t* xb, const float* wg, const float
 }
 
 // One warp per token: k rounds of a warp-wide arg-max (larger logit wins,
-// equal logits go to the lower expert id), then the softmax over the chosen k.
+// equal logits go to the lower expert id, NaN ranks last), then the softmax over
+// the chosen k (NaN weights where the logits were NaN or infinite).
 __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ logits, int64_t T, int E, int k,
                                                    int32_t* __restrict__ ids, float* __restrict__ w,
                                                    int32_t* __restrict__ counts) {
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ log
 #pragma unroll
     for (int q = 0; q < kMaxExperts / 32; ++q) {
         const int e = lane + 32 * q;
-        v[q] = (e < E) ? __ldg(logits + t * E + e) : 0.0f;
+        v[q] = (e < E) ? rankable(__ldg(logits + t * E + e)) : 0.0f;
     }
     uint32_t taken = 0;
     float sel_v[kMaxTopK];

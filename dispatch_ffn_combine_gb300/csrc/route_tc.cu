@@ -409,8 +409,10 @@ __global__ void __launch_bounds__(kSelThreads) route_select_kernel(
             if (e < E) {
                 const float a = __ldg(arow + e);
                 const float b = c_rel * nx * __ldg(wnorm + e) + c_abs * fabsf(a);
-                lo[q] = a - b;
-                up[q] = a + b;
+                // without an interval (NaN or infinities): a candidate, which fails its check below
+                const bool interval = fabsf(a - b) < __uint_as_float(0x7f800000u);
+                lo[q] = interval ? a - b : __uint_as_float(0xff800000u);
+                up[q] = interval ? a + b : __uint_as_float(0x7f800000u);
             }
         }
         // L: the k-th largest lower end
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(kSelThreads) route_select_kernel(
             int bi = kNone;
             for (int c = lane; c < nlist; c += 32) {
                 const int e = cand[c];
-                const float v = cval[c];
+                const float v = rankable(cval[c]);
                 bool used = false;
                 for (int jj = 0; jj < j; ++jj) used |= (sel_i[jj] == e);
                 if (!used && (bi == kNone || v > bv || (v == bv && e < bi))) {
