@@ -29,12 +29,14 @@
 // are a multiple of 8 apart, so that place, and with it the columns that a
 // thread holds, stay the same.
 //
-// Measured, of the measured copy rate: 32768 x 7168 bf16 forward 146 us (0.96),
-// backward 249 us (0.84); 16384 x 4096 fp32 with dres 95 us (0.63) and 211 us
-// (0.66); 16384 x 4095 bf16 70 us (0.57) and 121 us (0.50).  The backward pass is
-// held by instructions (22 per value, most of them unpacking and addresses) on
-// the 14 to 16 warps that its registers allow, the fp32 rows by 16-byte accesses
-// 32 bytes apart.
+// Measured, and the share of the measured copy rate: 32768 x 7168 bf16 forward
+// 146 us (0.96), backward 249 us (0.84); 16384 x 4096 fp32 forward 91 us (0.66),
+// backward with dres 211 us (0.66); 16384 x 4095 bf16 70 us (0.57) and 121 us
+// (0.50).  At 16384 x 7168 bf16 the backward kernel executes 20.7 instructions per
+// value (6.6 integer, 6.1 fp32) on the 14 warps of its 126 registers, with the
+// issue slots 53 % busy and DRAM at 45 %: it waits on instruction latency, more
+// than on memory.  Not measured: what holds the fp32 rows (a lane's 32 bytes are
+// two 16-byte accesses, each 32 bytes from the next lane's).
 #include <algorithm>
 #include <numeric>
 
