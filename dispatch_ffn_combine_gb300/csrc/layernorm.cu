@@ -209,6 +209,8 @@ struct Place {
         col = (warp - gid * warps) * (kLaneStep * nv) + 8 * (threadIdx.x & 31) - start;
         left = d - col;
     }
+    // The rows from this one on may share their last word with the tensor's end.
+    static __device__ __forceinline__ int near_end(int rows, int d) { return rows - 1 - 7 / d; }
     __device__ __forceinline__ int64_t first(int d) const { return static_cast<int64_t>(row0) * d + col; }
     __device__ __forceinline__ bool in(int v) const { return kLaneStep * v < left; }
     __device__ __forceinline__ bool whole(int v) const {
@@ -320,9 +322,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (kStages * X::kBytes) + (threadIdx.x & 31) * 16;
     const T* ahead = x + p.first(d);
     int row_ahead = p.row0;
+    const int near_end = p.near_end(rows, d);
     bf16* out = y + p.first(d);
     auto fetch = [&](uint32_t slot) {
-        if (row_ahead < rows) X::copy(mine + slot, ahead, p, row_ahead == rows - 1);
+        if (row_ahead < rows) X::copy(mine + slot, ahead, p, row_ahead >= near_end);
         ahead += stride;
         row_ahead += p.step;
         cp_async_commit();
@@ -397,9 +400,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (STAGES * stage_bytes) + (threadIdx.x & 31) * 16;
     int64_t at = p.first(d), ahead = at;
     int row_ahead = p.row0;
+    const int near_end = p.near_end(rows, d);
     auto fetch = [&](uint32_t slot) {
         if (row_ahead < rows) {
-            const bool last = row_ahead == rows - 1;
+            const bool last = row_ahead >= near_end;
             X::copy(mine + slot, x + ahead, p, last);
             Y::copy(mine + slot + X::kBytes, dy + ahead, p, last);
             if (dres != nullptr) X::copy(mine + slot + X::kBytes + Y::kBytes, dres + ahead, p, last);
