@@ -13,9 +13,9 @@
 // fp32 and rounded where it is stored.
 //
 // Both kernels are bound by HBM.  Blocks stay on their SM and walk over the
-// rows; each thread copies its own values of the next rows into shared memory
-// (cp.async) while the current row is reduced, so no barrier waits for memory
-// and a block holds two to three rows in flight.
+// rows; each warp copies its own values of the next rows into shared memory
+// (cp.async) while the current row is reduced, so no barrier between warps waits
+// for memory and a block holds two to three rows in flight.
 //
 // The backward pass reads x and dy once: each thread keeps its columns' dgamma
 // and dbeta in registers over the block's rows, the block writes one partial
@@ -30,13 +30,12 @@
 // thread holds, stay the same.
 //
 // Measured, and the share of the measured copy rate: 32768 x 7168 bf16 forward
-// 146 us (0.96), backward 249 us (0.84); 16384 x 4096 fp32 forward 91 us (0.66),
-// backward with dres 211 us (0.66); 16384 x 4095 bf16 70 us (0.57) and 121 us
-// (0.50).  At 16384 x 7168 bf16 the backward kernel executes 20.7 instructions per
+// 146 us (0.96), backward 249 us (0.84); 16384 x 4096 fp32 forward 66 us (0.91),
+// backward with dres 146 us (0.96); 16384 x 4095 bf16 70 us (0.57) and 123 us
+// (0.49).  At 16384 x 7168 bf16 the backward kernel executes 20.7 instructions per
 // value (6.6 integer, 6.1 fp32) on the 14 warps of its 126 registers, with the
 // issue slots 53 % busy and DRAM at 45 %: it waits on instruction latency, more
-// than on memory.  Not measured: what holds the fp32 rows (a lane's 32 bytes are
-// two 16-byte accesses, each 32 bytes from the next lane's).
+// than on memory.
 #include <algorithm>
 #include <numeric>
 
@@ -101,11 +100,18 @@ __device__ __forceinline__ void unpack(const uint4 (&w)[2], f2 (&f)[4]) {  // fp
     }
 }
 
-__device__ __forceinline__ void store8(bf16* p, const f2 (&f)[4]) {
+__device__ __forceinline__ void store8(bf16* p, const f2 (&f)[4], bool) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0].x(), f[0].y()), pack_bf16x2(f[1].x(), f[1].y()),
                                               pack_bf16x2(f[2].x(), f[2].y()), pack_bf16x2(f[3].x(), f[3].y()));
 }
-__device__ __forceinline__ void store8(float* p, const f2 (&f)[4]) {
+// One store of 32 bytes (whole sectors) where the tensor starts on a multiple of 32, else two.
+__device__ __forceinline__ void store8(float* p, const f2 (&f)[4], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0].x()), "f"(f[0].y()),
+                     "f"(f[1].x()), "f"(f[1].y()), "f"(f[2].x()), "f"(f[2].y()), "f"(f[3].x()), "f"(f[3].y())
+                     : "memory");
+        return;
+    }
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0].x(), f[0].y(), f[1].x(), f[1].y());
     reinterpret_cast<float4*>(p)[1] = make_float4(f[2].x(), f[2].y(), f[3].x(), f[3].y());
 }
@@ -187,8 +193,8 @@ struct GroupSum {
 // A warp owns 256 NV consecutive columns of its row; lane l's vector v is the
 // eight values from column 256 v + 8 l of them (shifted by the row's start in
 // its first word), so every offset below is a constant.  One stage of the ring
-// holds a row per group: per warp and tensor, NV vectors of 32 lanes, each
-// thread reading only what it copied itself.
+// holds a row per group: per warp and tensor, NV vectors of 32 lanes, read by the
+// warp that copied them.
 
 constexpr int kLaneStep = 256;  // columns between a lane's vectors
 
@@ -221,23 +227,26 @@ struct Place {
     }
     // Values outside the row become zero (NaN of another row included).
     __device__ __forceinline__ void mask(int v, f2 (&f)[4]) const {
-        if (kAligned || whole(v)) return;
+        if constexpr (!kAligned) {
+            if (whole(v)) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f[e] = f2(has(v, 2 * e) ? f[e].x() : 0.0f, has(v, 2 * e + 1) ? f[e].y() : 0.0f);
+            for (int e = 0; e < 4; ++e)
+                f[e] = f2(has(v, 2 * e) ? f[e].x() : 0.0f, has(v, 2 * e + 1) ? f[e].y() : 0.0f);
         }
     }
     // The row's values of vector v to p[0..7].
     template <typename T>
-    __device__ __forceinline__ void store(int v, T* p, const f2 (&f)[4]) const {
-        if (kAligned || whole(v)) {
-            store8(p, f);
-            return;
-        }
+    __device__ __forceinline__ void store(int v, T* p, const f2 (&f)[4], bool wide) const {
+        if constexpr (kAligned) {
+            store8(p, f, wide);
+        } else if (whole(v)) {
+            store8(p, f, wide);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (has(v, 2 * e)) store1(p + 2 * e, f[e].x());
-            if (has(v, 2 * e + 1)) store1(p + 2 * e + 1, f[e].y());
+            for (int e = 0; e < 4; ++e) {
+                if (has(v, 2 * e)) store1(p + 2 * e, f[e].x());
+                if (has(v, 2 * e + 1)) store1(p + 2 * e + 1, f[e].y());
+            }
         }
     }
     // The weights of vector v, zeros outside the row.  Away from the row's ends they are read
@@ -268,35 +277,57 @@ struct Place {
     }
 };
 
+// A warp's part of a ring stage for one tensor.  fp32: a lane's eight values are
+// two words; copied and read by that lane they would be accesses of 16 bytes, 32
+// apart (half of each sector, and two lanes on a bank).  So lane l copies words l
+// and 32 + l of a vector's 64, word w goes to place w ^ (w / 8 & 1), and the lane
+// that holds words 2l and 2l + 1 reads them without conflicts, after a warp barrier.
+// (16384 x 4096 forward 66 us, with each lane's own words 95; backward with dres
+// 146 and 214, there with dx in stores of 32 bytes, too.)
 template <typename T, int NV>
 struct RingPart {
     static constexpr int kW = kWords8<T>;
+    static constexpr bool kShared = kW > 1;         // a lane reads what others of its warp copied
     static constexpr int kWords = NV * kW * 32;     // 16-byte words per warp and stage
     static constexpr uint32_t kBytes = 16 * kWords;
 
-    // `slot`: shared address of this lane's first word; `row`: its first vector.
-    // The tensor's last word is read up to the tensor's end only.
+    // Bytes from a stage's start to the lane's first word, to copy and to read.
+    static __device__ __forceinline__ uint32_t copy_at() {
+        const uint32_t lane = threadIdx.x & 31;
+        return 16 * (kShared ? lane ^ (lane >> 3 & 1) : lane);
+    }
+    static __device__ __forceinline__ uint32_t read_at() {
+        const uint32_t lane = threadIdx.x & 31;
+        return kShared ? 32 * lane + 16 * (lane >> 2 & 1) : 16 * lane;
+    }
+    // Values that the word a lane copies first lies before the first that it holds.
+    static __device__ __forceinline__ int before() { return kShared ? 4 * (threadIdx.x & 31) : 0; }
+
+    // `slot`: shared address of the first word that this lane copies; `row`: where it lies in
+    // the row.  The tensor's last word is read up to the tensor's end only.
     template <bool kAligned>
     static __device__ __forceinline__ void copy(uint32_t slot, const T* row, const Place<kAligned>& p, bool last) {
+        const int left = p.left + before();
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (p.in(v)) {
+        for (int v = 0; v < NV; ++v) {
 #pragma unroll
-                for (int q = 0; q < kW; ++q) {
-                    const uint4* src = reinterpret_cast<const uint4*>(row + kLaneStep * v) + q;
-                    const uint32_t dst = slot + (v * kW + q) * 512;
-                    const int bytes = (p.left - kLaneStep * v) * static_cast<int>(sizeof(T)) - 16 * q;
-                    if (kAligned || !last || bytes >= 16)
-                        cp_async16_at(dst, src);
-                    else if (bytes > 0)
-                        cp_async16_part(dst, src, bytes);
-                }
+            for (int q = 0; q < kW; ++q) {
+                const int off = kLaneStep * v + 128 * q;
+                if (off >= left) continue;
+                const uint32_t dst = slot + (v * kW + q) * 512;
+                const int bytes = (left - off) * static_cast<int>(sizeof(T));
+                if (kAligned || !last || bytes >= 16)
+                    cp_async16_at(dst, row + off);
+                else
+                    cp_async16_part(dst, row + off, bytes);
             }
+        }
     }
+    // `slot`: shared address of the first word that this lane reads.
     static __device__ __forceinline__ void read(uint32_t slot, int v, f2 (&f)[4]) {
         uint4 w[kW];
 #pragma unroll
-        for (int q = 0; q < kW; ++q) w[q] = ld_shared16(slot + (v * kW + q) * 512);
+        for (int q = 0; q < kW; ++q) w[q] = ld_shared16((q == 0 ? slot : slot ^ 16) + v * kW * 512);
         unpack(w, f);
     }
 };
@@ -307,7 +338,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
                      int rows, int d, float eps, int warps, bf16* __restrict__ y, float* __restrict__ mean,
                      float* __restrict__ rstd) {
     using X = RingPart<T, NV>;
-    extern __shared__ uint4 ring[];
+    extern __shared__ __align__(32) uint4 ring[];
     __shared__ float red[GroupSum<1>::kWords];
     const Place<kAligned> p(d, warps, NV);
     const GroupSum<1> group_sum(smem_u32(red), warps, p.gid);
@@ -319,13 +350,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
         p.weights(gamma, v, g[v]);
         p.weights(beta, v, b[v]);
     }
-    const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (kStages * X::kBytes) + (threadIdx.x & 31) * 16;
-    const T* ahead = x + p.first(d);
+    const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (kStages * X::kBytes);
+    const uint32_t to = mine + X::copy_at(), from = mine + X::read_at();
+    const T* ahead = x + p.first(d) - X::before();
     int row_ahead = p.row0;
     const int near_end = p.near_end(rows, d);
     bf16* out = y + p.first(d);
     auto fetch = [&](uint32_t slot) {
-        if (row_ahead < rows) X::copy(mine + slot, ahead, p, row_ahead >= near_end);
+        if (row_ahead < rows) X::copy(to + slot, ahead, p, row_ahead >= near_end);
         ahead += stride;
         row_ahead += p.step;
         cp_async_commit();
@@ -336,7 +368,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     for (int row = p.row0; row < rows; row += p.step, out += stride) {
         fetch(slot == 0 ? (kStages - 1) * X::kBytes : slot - X::kBytes);
         cp_async_wait<kStages - 1>();
-        const uint32_t stage = after(mine + slot);
+        if (X::kShared) __syncwarp();
+        const uint32_t stage = after(from + slot);
         f2 f[NV][4], s = both(0.0f), s2 = both(0.0f);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -374,7 +407,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
             if (p.in(v)) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f[v][e] = fma2(mul2(f[v][e], both(rs)), g[v][e], b[v][e]);
-                p.store(v, out + kLaneStep * v, f[v]);
+                p.store(v, out + kLaneStep * v, f[v], false);
             }
     }
 }
@@ -390,23 +423,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     using X = RingPart<T, NV>;
     using Y = RingPart<bf16, NV>;
     constexpr bool kHold = NV == 2;
-    extern __shared__ uint4 ring[];
+    extern __shared__ __align__(32) uint4 ring[];
     __shared__ float red[GroupSum<2>::kWords];
     const Place<kAligned> p(d, warps, NV);
     const GroupSum<2> group_sum(smem_u32(red), warps, p.gid);
     const uint32_t stage_bytes = X::kBytes + Y::kBytes + (dres != nullptr ? X::kBytes : 0);
     const float inv_d = 1.0f / static_cast<float>(d);
+    const bool wide = (reinterpret_cast<uintptr_t>(dx) & 31) == 0;
     const int64_t stride = static_cast<int64_t>(p.step) * d;
-    const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (STAGES * stage_bytes) + (threadIdx.x & 31) * 16;
+    const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (STAGES * stage_bytes);
+    const uint32_t to = mine + X::copy_at(), from = mine + X::read_at();
+    const uint32_t y_to = X::kBytes + Y::copy_at() - X::copy_at(), y_from = X::kBytes + Y::read_at() - X::read_at();
     int64_t at = p.first(d), ahead = at;
     int row_ahead = p.row0;
     const int near_end = p.near_end(rows, d);
     auto fetch = [&](uint32_t slot) {
         if (row_ahead < rows) {
             const bool last = row_ahead >= near_end;
-            X::copy(mine + slot, x + ahead, p, last);
-            Y::copy(mine + slot + X::kBytes, dy + ahead, p, last);
-            if (dres != nullptr) X::copy(mine + slot + X::kBytes + Y::kBytes, dres + ahead, p, last);
+            X::copy(to + slot, x + ahead - X::before(), p, last);
+            Y::copy(to + slot + y_to, dy + ahead, p, last);
+            if (dres != nullptr) X::copy(to + slot + X::kBytes + Y::kBytes, dres + ahead - X::before(), p, last);
         }
         ahead += stride;
         row_ahead += p.step;
@@ -426,11 +462,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     int buffer = 0;
     float r_next = p.row0 < rows ? __ldg(rstd + p.row0) : 0.0f, m_next = p.row0 < rows ? __ldg(mean + p.row0) : 0.0f;
     for (int row = p.row0; row < rows; row += p.step, at += stride) {
+        if (X::kShared) __syncwarp();  // the slot was read by all lanes
         fetch(slot == 0 ? last_slot : slot - stage_bytes);
         const float r = r_next, m = -m_next;
         if (row + p.step < rows) r_next = __ldg(rstd + row + p.step), m_next = __ldg(mean + row + p.step);
         cp_async_wait<STAGES - 1>();
-        uint32_t stage = after(mine + slot);
+        if (X::kShared) __syncwarp();
+        uint32_t stage = after(from + slot);
         slot = slot == last_slot ? 0 : slot + stage_bytes;
         f2 st = both(0.0f), sc = both(0.0f);  // sums of r t and r t (x - mean)
         f2 cv[kHold ? NV : 1][4], tv[kHold ? NV : 1][4];  // x - mean, then r t
@@ -440,7 +478,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
                 f2 (&c)[4] = cv[kHold ? v : 0];
                 f2 y[4];
                 X::read(stage, v, c);
-                Y::read(stage + X::kBytes, v, y);
+                Y::read(stage + y_from, v, y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) c[e] = add2(c[e], both(m));
                 p.mask(v, c);
@@ -469,7 +507,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
                 f2 y[4];
                 if (!kHold) {
                     X::read(stage, v, c);
-                    Y::read(stage + X::kBytes, v, y);
+                    Y::read(stage + y_from, v, y);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -480,7 +518,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) c[e] = add2(c[e], y[e]);
                 }
-                p.store(v, dx + at + kLaneStep * v, c);
+                p.store(v, dx + at + kLaneStep * v, c, wide);
             }
     }
     pdl_launch_dependents();  // the kernel that adds the partial rows

@@ -380,6 +380,37 @@ def test_layernorm_many_rows_repeat():
     _close(a[2], wb, T * 2.0 ** -23 * dy.to(F64).abs().sum(0), "fp32 dbeta")
 
 
+@pytest.mark.parametrize("d", [3, 1001, 2048, 12288])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_layernorm_tensors_on_odd_multiples_of_16_bytes(d, dtype):
+    """Tensors that start 16 bytes past a multiple of 32, between NaNs: the same arithmetic, so the
+    same bits as for tensors on a multiple of 32, and nothing written around the outputs."""
+    T = 13
+
+    def inside(src):  # the same values, 16 bytes into a buffer of NaNs
+        pad = 16 // src.element_size()
+        buf = torch.full((src.numel() + 2 * pad,), float("nan"), dtype=src.dtype, device=DEV)
+        view = buf[pad:pad + src.numel()].view(src.shape)
+        view.copy_(src)
+        assert view.data_ptr() % 32 == 16
+        return buf, view
+
+    x, dy, dres = _randn((T, d), 1, 2.0, dtype), _randn((T, d), 2), _randn((T, d), 3, 1.0, dtype)
+    gamma, beta = 1 + _randn((d,), 4, 0.1, torch.float32), _randn((d,), 5, 0.1, torch.float32)
+    y, mean, rstd = mk.mk_moe_layernorm(x, gamma, beta)
+    dx, dgamma, dbeta = mk.mk_moe_layernorm_bwd(dy, x, gamma, mean, rstd, dres=dres)
+    (_, x2), (_, dy2), (_, dres2) = inside(x), inside(dy), inside(dres)
+    (_, gamma2), (_, beta2) = inside(gamma), inside(beta)
+    (ybuf, y2), (dxbuf, dx2) = inside(torch.zeros_like(y)), inside(torch.zeros_like(dx))
+    mk.mk_moe_layernorm(x2, gamma2, beta2, y=y2, mean=mean, rstd=rstd)
+    _, dgamma2, dbeta2 = mk.mk_moe_layernorm_bwd(dy2, x2, gamma2, mean, rstd, dres=dres2, dx=dx2)
+    for got, want in ((y2, y), (dx2, dx), (dgamma2, dgamma), (dbeta2, dbeta)):
+        assert torch.equal(got, want)
+    for buf, t in ((ybuf, y), (dxbuf, dx)):
+        pad = 16 // t.element_size()
+        assert bool(torch.isnan(buf[:pad]).all()) and bool(torch.isnan(buf[pad + t.numel():]).all())
+
+
 def test_layernorm_constant_rows_and_no_rows():
     """A constant row has variance zero: y = beta, finite gradients; no rows give zero weight gradients."""
     d = 96
