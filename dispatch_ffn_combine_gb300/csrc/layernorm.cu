@@ -34,8 +34,9 @@
 // backward with dres 146 us (0.96); 16384 x 4095 bf16 70 us (0.57) and 123 us
 // (0.49).  At 16384 x 7168 bf16 the backward kernel executes 20.7 instructions per
 // value (6.6 integer, 6.1 fp32) on the 14 warps of its 126 registers, with the
-// issue slots 53 % busy and DRAM at 45 %: it waits on instruction latency, more
-// than on memory.
+// issue slots 50 % busy and DRAM at 67 %; per instruction a warp waits 1.25 cycles
+// on fixed latencies, 1.16 on shared memory and shuffles, 0.94 at the row's
+// barrier and 0.60 on global memory.
 #include <algorithm>
 #include <numeric>
 
