@@ -49,7 +49,8 @@
 // skewed rows over 64 experts of 1536 x 4096 fp32 980 us (0.86 R), adding 1210
 // (0.69 R: the additions read the gradient too, 1.6 GB); 16384 rows over
 // 32 of 1408 x 2048 fp32 105 us (0.68 C), adding 141 (0.90 C), bf16 88 (0.55 R);
-// 8191 rows over 256 of them, bf16 302 us (0.76 C), fp32 adding 880 (1.01 C).
+// 8191 rows over 256 of them, bf16 302 us (0.76 C; the MMA warp and the epilogue
+// wait on each other for accumulators, not for stores), fp32 adding 880 (1.01 C).
 //
 // Every wait is bounded, as in the other pair kernels.
 #include <algorithm>
