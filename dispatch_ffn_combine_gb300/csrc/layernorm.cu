@@ -201,11 +201,13 @@ constexpr int kLaneStep = 256;  // columns between a lane's vectors
 
 // Where a thread stands: its row group, its first vector's first column (from
 // -7: the first word may start in the row before), and its group's rows row0,
-// row0 + step, ... below `rows`.  kAligned: d is a multiple of 8, every row
-// starts a word.
+// row0 + step, ... below `rows`.  Rows are counted without a sign: a group looks up
+// to three steps (of 16 rows per block) past the last of up to 2^31 - 1 rows.
+// kAligned: d is a multiple of 8, every row starts a word.
 template <bool kAligned>
 struct Place {
-    int gid, col, left, row0, step;  // left: columns from the first vector to the row's end
+    int gid, col, left;  // left: columns from the first vector to the row's end
+    uint32_t row0, step;
     __device__ __forceinline__ Place(int d, int warps, int nv) {
         const int warp = threadIdx.x >> 5;
         const int groups = (blockDim.x >> 5) / warps;
@@ -217,7 +219,7 @@ struct Place {
         left = d - col;
     }
     // The rows from this one on may share their last word with the tensor's end.
-    static __device__ __forceinline__ int near_end(int rows, int d) { return rows - 1 - 7 / d; }
+    static __device__ __forceinline__ uint32_t near_end(uint32_t rows, int d) { return rows - min(rows, 1u + 7u / d); }
     __device__ __forceinline__ int64_t first(int d) const { return static_cast<int64_t>(row0) * d + col; }
     __device__ __forceinline__ bool in(int v) const { return kLaneStep * v < left; }
     __device__ __forceinline__ bool whole(int v) const {
@@ -336,7 +338,7 @@ struct RingPart {
 template <typename T, int NV, bool kAligned>
 __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     layernorm_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
-                     int rows, int d, float eps, int warps, bf16* __restrict__ y, float* __restrict__ mean,
+                     uint32_t rows, int d, float eps, int warps, bf16* __restrict__ y, float* __restrict__ mean,
                      float* __restrict__ rstd) {
     using X = RingPart<T, NV>;
     extern __shared__ __align__(32) uint4 ring[];
@@ -354,8 +356,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     const uint32_t mine = smem_u32(ring) + (threadIdx.x >> 5) * (kStages * X::kBytes);
     const uint32_t to = mine + X::copy_at(), from = mine + X::read_at();
     const T* ahead = x + p.first(d) - X::before();
-    int row_ahead = p.row0;
-    const int near_end = p.near_end(rows, d);
+    uint32_t row_ahead = p.row0;
+    const uint32_t near_end = p.near_end(rows, d);
     bf16* out = y + p.first(d);
     auto fetch = [&](uint32_t slot) {
         if (row_ahead < rows) X::copy(to + slot, ahead, p, row_ahead >= near_end);
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i * X::kBytes);
     uint32_t slot = 0;
-    for (int row = p.row0; row < rows; row += p.step, out += stride) {
+    for (uint32_t row = p.row0; row < rows; row += p.step, out += stride) {
         fetch(slot == 0 ? (kStages - 1) * X::kBytes : slot - X::kBytes);
         cp_async_wait<kStages - 1>();
         if (X::kShared) __syncwarp();
@@ -420,7 +422,7 @@ template <typename T, int NV, bool kAligned, int STAGES>
 __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     layernorm_bwd_kernel(const bf16* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ gamma,
                          const float* __restrict__ mean, const float* __restrict__ rstd, const T* __restrict__ dres,
-                         int rows, int d, int warps, T* __restrict__ dx, float* __restrict__ part) {
+                         uint32_t rows, int d, int warps, T* __restrict__ dx, float* __restrict__ part) {
     using X = RingPart<T, NV>;
     using Y = RingPart<bf16, NV>;
     constexpr bool kHold = NV == 2;
@@ -436,8 +438,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     const uint32_t to = mine + X::copy_at(), from = mine + X::read_at();
     const uint32_t y_to = X::kBytes + Y::copy_at() - X::copy_at(), y_from = X::kBytes + Y::read_at() - X::read_at();
     int64_t at = p.first(d), ahead = at;
-    int row_ahead = p.row0;
-    const int near_end = p.near_end(rows, d);
+    uint32_t row_ahead = p.row0;
+    const uint32_t near_end = p.near_end(rows, d);
     auto fetch = [&](uint32_t slot) {
         if (row_ahead < rows) {
             const bool last = row_ahead >= near_end;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, NV == 1 ? 2 : 1)
     uint32_t slot = 0;
     int buffer = 0;
     float r_next = p.row0 < rows ? __ldg(rstd + p.row0) : 0.0f, m_next = p.row0 < rows ? __ldg(mean + p.row0) : 0.0f;
-    for (int row = p.row0; row < rows; row += p.step, at += stride) {
+    for (uint32_t row = p.row0; row < rows; row += p.step, at += stride) {
         if (X::kShared) __syncwarp();  // the slot was read by all lanes
         fetch(slot == 0 ? last_slot : slot - stage_bytes);
         const float r = r_next, m = -m_next;
