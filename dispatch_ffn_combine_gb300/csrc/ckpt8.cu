@@ -140,8 +140,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_ckpt8_bwd_kernel(
     if (row_ok) {
         const int64_t base = row * f;
         const float w = row_weight != nullptr ? __ldg(row_weight + row) : 1.0f;
+        // without a sign: c passes f, which may be 2^31 - 64, by up to 2048
 #pragma unroll 2
-        for (int c = ((warp % WPR) * 32 + lane) * 8; c < f; c += WPR * 256) {
+        for (uint32_t c = ((warp % WPR) * 32 + lane) * 8; c < static_cast<uint32_t>(f); c += WPR * 256) {
             const int64_t at = base + c;
             const uint4 dv = __ldcs(reinterpret_cast<const uint4*>(dh + at));
             const uint2 gc = __ldcs(reinterpret_cast<const uint2*>(codes + at));

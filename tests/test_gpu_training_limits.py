@@ -84,3 +84,32 @@ def test_layernorm_with_the_most_rows():
         sg = sg + (dy[a:b].to(F64).abs() * err).sum(0) + 25000 * 2.0 ** -23 * (dy[a:b].to(F64) * xh).abs().sum(0)
         sb = sb + 25000 * 2.0 ** -23 * dy[a:b].to(F64).abs().sum(0)
     assert bool(((dgamma - wg).abs() <= sg).all()) and bool(((dbeta - wb).abs() <= sb).all())
+
+
+def test_swiglu_with_the_longest_row():
+    """One row of 2^31 - 64 values: each is computed on its own, so a row that repeats a short one gives the
+    short one's outputs over and over, bit for bit, and nothing outside the outputs is written."""
+    _room(60)
+    f = (1 << 31) - 64
+    short = 64 * 31 * 601
+    times = f // short
+    assert times * short == f
+    gate, up, dh = ((2 * torch.randn((1, short), generator=torch.Generator().manual_seed(i))).to(BF).to(DEV)
+                    for i in range(3))
+    w = torch.tensor([0.75], device=DEV)
+    h, codes, scales = mk.mk_moe_swiglu_ckpt8(gate, up)
+    want = mk.mk_moe_swiglu_ckpt8_bwd(dh, codes, scales, w)
+    long_gate, long_up = gate.repeat(1, times), up.repeat(1, times)
+    long_h, long_codes, long_scales = mk.mk_moe_swiglu_ckpt8(long_gate, long_up)
+    assert bool((long_h.view(times, short) == h).all())
+    for got, one in ((long_codes, codes), (long_scales, scales)):
+        for plane in range(2):
+            assert bool((got[plane].view(times, -1) == one[plane]).all())
+    del long_gate, long_up, long_h
+    outs = [_guarded((1, f), BF) for _ in range(3)]
+    drow = mk.mk_moe_swiglu_ckpt8_bwd(dh.repeat(1, times), long_codes, long_scales, w, dgate=outs[0][1],
+                                      dup=outs[1][1], hw=outs[2][1])[3]
+    for (buf, t), one in zip(outs, want):
+        assert _untouched(buf)
+        assert bool((t.view(times, short) == one).all())
+    assert bool(torch.isfinite(drow).all())
