@@ -524,6 +524,10 @@ def mk_moe_ep_regroup(rows_in, counts, to_expert_major, rows_out=None, expert_of
 # These calls are short on small batches (a few microseconds on the GPU), so
 # their bindings check every argument with one pass over plain attributes and
 # pass addresses as integers.
+#
+# stream: the call runs there, behind what is queued on it.  The inputs have to
+# be ready on that stream, and a caller that goes on with the results on another
+# stream makes it wait, as for any work on two streams.
 
 MK_TYPE_BF16 = 0
 MK_TYPE_FP32 = 1
@@ -554,23 +558,34 @@ def _inputs(like, *wanted):
         raise ValueError(f"{name} must be on {like.device}, got {t.device}")
 
 
-def _new(t, dtype, shape, like, stream):
-    """The output or workspace that was passed, or a new one.
+def _empty(dtype, shape, like, stream):
+    """New memory for the call's stream (None: the current one), from that stream's pool.
 
-    A new tensor belongs to the current stream's memory; where the call runs on
-    another one, the allocator is told, so that the memory is not handed out
-    again before that stream is done with it."""
+    There the allocator hands out a freed block only behind the work that used it.  A block
+    from the current stream's pool may still be in use by kernels queued on the current stream,
+    which another one does not wait for."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+
+
+def _new(t, dtype, shape, like, stream):
+    """The output that was passed, or a new one.
+
+    The caller goes on with it on the current stream, so the allocator is told: the memory is
+    not handed out again before that stream is done with it either."""
     if t is not None:
         return t
-    t = torch.empty(*shape, dtype=dtype, device=like.device)
+    t = _empty(dtype, shape, like, stream)
     if stream is not None:
-        t.record_stream(stream)
+        t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
 def _workspace(ws, nbytes, like, stream):
     if ws is None:
-        return _new(None, _U8, (nbytes,), like, stream)
+        return _empty(_U8, (nbytes,), like, stream)
     if not isinstance(ws, torch.Tensor) or ws.dtype != _U8 or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous CUDA tensor of bytes")
     if ws.device != like.device:
@@ -635,7 +650,7 @@ def mk_moe_grouped_wgrad(dout, expert_offsets, x_perm, dw=None, accumulate=False
     dw = _new(dw, dtype, (E, n, d), dout, stream)
     if ws is None:
         nbytes = (_lib or load_library()).mk_moe_grouped_wgrad_workspace_size(S, d, E, n)
-        ws = _new(None, _U8, (max(nbytes, 256),), dout, stream)
+        ws = _empty(_U8, (max(nbytes, 256),), dout, stream)
     ws = _workspace(ws, 256, dout, stream)
     _run("mk_moe_grouped_wgrad", dout, stream, dout.data_ptr(), expert_offsets.data_ptr(), x_perm.data_ptr(), S, d, E,
          n, dw.data_ptr(), _TYPES[dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel())
