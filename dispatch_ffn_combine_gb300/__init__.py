@@ -8,9 +8,14 @@ not sm_103, calls raise.
 
     import dispatch_ffn_combine_gb300 as mk
     y = mk.mk_moe_layer(x, wg, bias, w1, w3, w2, k)      # torch CUDA tensors
+
+``stream``: a call runs there, behind what is queued on it (default: the current
+stream).  Its inputs have to be ready on that stream, and a caller that goes on
+with the results on another one makes that stream wait, as for any work on two.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -158,6 +163,43 @@ def _need(t, dtype, shape, name, device=True):
     return t
 
 
+def _pool(stream):
+    """Allocations inside come from the pool of the call's stream (None: the current one).
+
+    There the allocator hands out a freed block only behind the work that used it.  A block
+    from the current stream's pool may still be in use by kernels queued on the current stream,
+    which another one does not wait for."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(dtype, shape, like, stream):
+    """New memory for the call's stream."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+    with _pool(stream):
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+
+
+def _new(t, dtype, shape, like, stream):
+    """The output that was passed, or a new one.
+
+    The caller goes on with it on the current stream, so the allocator is told: the memory is
+    not handed out again before that stream is done with it either."""
+    if t is not None:
+        return t
+    t = _empty(dtype, shape, like, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _outputs(out, wanted, like, stream):
+    """The tensors of the dict `out` (or None), and new ones for the names of `wanted` that it lacks."""
+    out = out or {}
+    return {name: out[name] if name in out else _new(None, dtype, shape, like, stream)
+            for name, (dtype, shape) in wanted.items()}
+
+
 def workspace_size(T: int, d: int, E: int, k: int, ffn: int) -> int:
     return int(load_library().mk_moe_workspace_size(T, d, E, k, ffn))
 
@@ -169,6 +211,13 @@ def alloc_workspace(T: int, d: int, E: int, k: int, ffn: int, device="cuda") -> 
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _layer_workspace(ws, T, d, E, k, ffn, like, stream):
+    if ws is not None:
+        return ws
+    with _pool(stream):
+        return alloc_workspace(T, d, E, k, ffn, like.device)
+
+
 def mk_moe_route(x, wg, bias, k, topk_ids=None, topk_w=None, expert_counts=None, ws=None, stream=None):
     """Router: returns (topk_ids [T,k] int32, topk_w [T,k] fp32, expert_counts [E] int32)."""
     T, d = x.shape
@@ -177,11 +226,10 @@ def mk_moe_route(x, wg, bias, k, topk_ids=None, topk_w=None, expert_counts=None,
     _need(wg, torch.float32, (E, d), "wg")
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
-    dev = x.device
-    topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    expert_counts = torch.empty(E, dtype=torch.int32, device=dev) if expert_counts is None else expert_counts
-    ws = alloc_workspace(T, d, E, k, 64, dev) if ws is None else ws
+    topk_ids = _new(topk_ids, torch.int32, (T, k), x, stream)
+    topk_w = _new(topk_w, torch.float32, (T, k), x, stream)
+    expert_counts = _new(expert_counts, torch.int32, (E,), x, stream)
+    ws = _layer_workspace(ws, T, d, E, k, 64, x, stream)
     st = load_library().mk_moe_route(_p(x), _p(wg), _p(bias), T, d, E, k, _p(topk_ids), _p(topk_w),
                                      _p(expert_counts), _p(ws), ws.numel(), _stream(stream))
     _check(st, "mk_moe_route")
@@ -216,16 +264,10 @@ def mk_moe_dispatch(x, topk_ids, topk_w, E, ws=None, stream=None, out=None):
     _need(topk_ids, torch.int32, (T, k), "topk_ids")
     if topk_w is not None:
         _need(topk_w, torch.float32, (T, k), "topk_w")
-    dev = x.device
-    o = out or {}
-    res = {
-        "expert_offsets": o.get("expert_offsets", torch.empty(E + 1, dtype=torch.int32, device=dev)),
-        "row_token": o.get("row_token", torch.empty(T * k, dtype=torch.int32, device=dev)),
-        "row_weight": o.get("row_weight", torch.empty(T * k, dtype=torch.float32, device=dev)),
-        "slot_row": o.get("slot_row", torch.empty((T, k), dtype=torch.int32, device=dev)),
-        "x_perm": o.get("x_perm", torch.empty((T * k, d), dtype=torch.bfloat16, device=dev)),
-    }
-    ws = alloc_workspace(T, d, E, k, 64, dev) if ws is None else ws
+    res = _outputs(out, {"expert_offsets": (torch.int32, (E + 1,)), "row_token": (torch.int32, (T * k,)),
+                         "row_weight": (torch.float32, (T * k,)), "slot_row": (torch.int32, (T, k)),
+                         "x_perm": (torch.bfloat16, (T * k, d))}, x, stream)
+    ws = _layer_workspace(ws, T, d, E, k, 64, x, stream)
     st = load_library().mk_moe_dispatch(_p(x), _p(topk_ids), _p(topk_w), T, d, E, k, _p(res["expert_offsets"]),
                                         _p(res["row_token"]), _p(res["row_weight"]), _p(res["slot_row"]),
                                         _p(res["x_perm"]), _p(ws), ws.numel(), _stream(stream))
@@ -244,10 +286,9 @@ def mk_moe_expert_ffn(x_perm, expert_offsets, row_weight, w1, w3, w2, h=None, P=
     _need(w1, torch.bfloat16, (E, f, d), "w1")
     _need(w3, torch.bfloat16, (E, f, d), "w3")
     _need(w2, torch.bfloat16, (E, d, f), "w2")
-    dev = x_perm.device
-    h = torch.empty((S, f), dtype=torch.bfloat16, device=dev) if h is None else h
-    P = torch.empty((S, d), dtype=torch.bfloat16, device=dev) if P is None else P
-    ws = torch.empty(256 + 4 * (E + 1), dtype=torch.uint8, device=dev) if ws is None else ws
+    h = _new(h, torch.bfloat16, (S, f), x_perm, stream)
+    P = _new(P, torch.bfloat16, (S, d), x_perm, stream)
+    ws = _empty(torch.uint8, (256 + 4 * (E + 1),), x_perm, stream) if ws is None else ws
     st = load_library().mk_moe_expert_ffn(_p(x_perm), _p(expert_offsets), _p(row_weight), _p(w1), _p(w3), _p(w2),
                                           S, d, E, f, _p(h), _p(P), _p(ws), ws.numel(), _stream(stream))
     _check(st, "mk_moe_expert_ffn")
@@ -264,10 +305,9 @@ def mk_moe_grouped_gemm(x_perm, expert_offsets, w, row_weight=None, out=None, ws
     _need(w, torch.bfloat16, (E, n, d), "w")
     if row_weight is not None:
         _need(row_weight, torch.float32, (S,), "row_weight")
-    dev = x_perm.device
-    out = torch.empty((S, n), dtype=torch.bfloat16, device=dev) if out is None else out
+    out = _new(out, torch.bfloat16, (S, n), x_perm, stream)
     _need(out, torch.bfloat16, (S, n), "out")
-    ws = torch.empty(256 + 4 * (E + 1), dtype=torch.uint8, device=dev) if ws is None else ws
+    ws = _empty(torch.uint8, (256 + 4 * (E + 1),), x_perm, stream) if ws is None else ws
     st = load_library().mk_moe_grouped_gemm(_p(x_perm), _p(expert_offsets), _p(row_weight), _p(w), S, d, E, n,
                                             _p(out), _p(ws), ws.numel(), _stream(stream))
     _check(st, "mk_moe_grouped_gemm")
@@ -297,17 +337,15 @@ def mk_moe_dispatch_gemm(x, wg, bias, w, k, out=None, ws=None, stream=None, row_
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     _need(w, torch.bfloat16, (E, n, d), "w")
-    dev = x.device
-    o = out or {}
-    res = {
-        "out": o.get("out", torch.empty((T * k, n), dtype=torch.bfloat16, device=dev)),
-        "expert_offsets": o.get("expert_offsets", torch.empty(E + 1, dtype=torch.int32, device=dev)),
-        "row_token": o.get("row_token", torch.empty(T * k, dtype=torch.int32, device=dev)),
-        "row_weight": (o.get("row_weight", torch.empty(T * k, dtype=torch.float32, device=dev))
-                       if row_weight else None),
-    }
+    wanted = {"out": (torch.bfloat16, (T * k, n)), "expert_offsets": (torch.int32, (E + 1,)),
+              "row_token": (torch.int32, (T * k,)), "row_weight": (torch.float32, (T * k,))}
+    if not row_weight:
+        del wanted["row_weight"]
+    res = {"row_weight": None, **_outputs(out, wanted, x, stream)}
     _need(res["out"], torch.bfloat16, (T * k, n), "out")
-    ws = alloc_dispatch_gemm_workspace(T, d, E, k, dev) if ws is None else ws
+    if ws is None:
+        with _pool(stream):
+            ws = alloc_dispatch_gemm_workspace(T, d, E, k, x.device)
     st = load_library().mk_moe_dispatch_gemm(_p(x), _p(wg), _p(bias), _p(w), T, d, E, k, n, _p(res["out"]),
                                              _p(res["expert_offsets"]), _p(res["row_token"]), _p(res["row_weight"]),
                                              _p(ws), ws.numel(), _stream(stream))
@@ -321,7 +359,7 @@ def mk_moe_combine(P, slot_row, y=None, stream=None):
     d = P.shape[1]
     _need(P, torch.bfloat16, (T * k, d), "P")
     _need(slot_row, torch.int32, (T, k), "slot_row")
-    y = torch.empty((T, d), dtype=torch.bfloat16, device=P.device) if y is None else y
+    y = _new(y, torch.bfloat16, (T, d), P, stream)
     st = load_library().mk_moe_combine(_p(P), _p(slot_row), T, d, k, _p(y), _stream(stream))
     _check(st, "mk_moe_combine")
     return y
@@ -374,8 +412,8 @@ def mk_moe_layer(x, wg, bias, w1, w3, w2, k, y=None, ws=None, phase_events=None,
     semaphores).  mover_ctas: fused-path SM split, 0 = adaptive.  gather_rows:
     kernel-per-step path, gemm1 gathers its rows from x (no dispatched copy)."""
     T, d, E, f = _layer_shapes(x, wg, bias, w1, w3, w2)
-    y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device) if y is None else y
-    ws = alloc_workspace(T, d, E, k, f, x.device) if ws is None else ws
+    y = _new(y, torch.bfloat16, (T, d), x, stream)
+    ws = _layer_workspace(ws, T, d, E, k, f, x, stream)
     st = load_library().mk_moe_layer(_p(x), _p(wg), _p(bias), _p(w1), _p(w3), _p(w2), T, d, E, k, f, _p(y), _p(ws),
                                      ws.numel(),
                                      _opts(phase_events, timeout_ns, inject, path, mover_ctas, trace, gather_rows),
@@ -432,7 +470,7 @@ def mk_moe_route_fallbacks(ws, stream=None):
 
 def mk_moe_route_approx_logits(ws, T, d, E, k, stream=None):
     """The approximate logits [T, E] fp32 the last candidate-filter router run on ws left there."""
-    out = torch.empty((T, E), dtype=torch.float32, device=ws.device)
+    out = _new(None, torch.float32, (T, E), ws, stream)
     _check(load_library().mk_moe_route_approx_logits(_p(ws), T, d, E, k, _p(out), _stream(stream)),
            "mk_moe_route_approx_logits")
     return out
@@ -451,11 +489,10 @@ TRACE_KINDS = {2: "route", 3: "dispatch", 5: "combine", 6: "gemm"}
 
 def mk_moe_layer_routing(ws, T, d, E, k, ffn, stream=None):
     """Routing tables the last mk_moe_layer call left in ws: (ids, w, offsets, slot_row)."""
-    dev = ws.device
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    off = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    slot = torch.empty((T, k), dtype=torch.int32, device=dev)
+    ids = _new(None, torch.int32, (T, k), ws, stream)
+    w = _new(None, torch.float32, (T, k), ws, stream)
+    off = _new(None, torch.int32, (E + 1,), ws, stream)
+    slot = _new(None, torch.int32, (T, k), ws, stream)
     st = load_library().mk_moe_layer_routing(_p(ws), T, d, E, k, ffn, _p(ids), _p(w), _p(off), _p(slot),
                                              _stream(stream))
     _check(st, "mk_moe_layer_routing")
@@ -504,14 +541,14 @@ def mk_moe_ep_regroup(rows_in, counts, to_expert_major, rows_out=None, expert_of
         raise ValueError("rows_in must be a contiguous CUDA tensor")
     rows = rows_in.shape[0]
     row_bytes = math.prod(rows_in.shape[1:]) * rows_in.element_size()
-    rows_out = torch.empty_like(rows_in) if rows_out is None else rows_out
+    rows_out = _new(rows_out, rows_in.dtype, rows_in.shape, rows_in, stream)
     if expert_offsets is not None:
         _need(expert_offsets, torch.int32, (El + 1,), "expert_offsets")
     if ws is None:
         n = int(load_library().mk_moe_ep_regroup_workspace_size(G, El))
         if n == 0:
             raise ValueError("invalid G, E_local for the regroup")
-        ws = torch.empty(n, dtype=torch.uint8, device=rows_in.device)
+        ws = _empty(torch.uint8, (n,), rows_in, stream)
     st = load_library().mk_moe_ep_regroup(_p(rows_in), _p(rows_out), _p(counts), G, El, rows, row_bytes,
                                           1 if to_expert_major else 0, _p(expert_offsets), _p(ws), ws.numel(),
                                           _stream(stream))
@@ -524,10 +561,6 @@ def mk_moe_ep_regroup(rows_in, counts, to_expert_major, rows_out=None, expert_of
 # These calls are short on small batches (a few microseconds on the GPU), so
 # their bindings check every argument with one pass over plain attributes and
 # pass addresses as integers.
-#
-# stream: the call runs there, behind what is queued on it.  The inputs have to
-# be ready on that stream, and a caller that goes on with the results on another
-# stream makes it wait, as for any work on two streams.
 
 MK_TYPE_BF16 = 0
 MK_TYPE_FP32 = 1
@@ -556,31 +589,6 @@ def _inputs(like, *wanted):
             pass
         _need(t, dtype, shape, name)  # says what is wrong
         raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-
-
-def _empty(dtype, shape, like, stream):
-    """New memory for the call's stream (None: the current one), from that stream's pool.
-
-    There the allocator hands out a freed block only behind the work that used it.  A block
-    from the current stream's pool may still be in use by kernels queued on the current stream,
-    which another one does not wait for."""
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=like.device)
-
-
-def _new(t, dtype, shape, like, stream):
-    """The output that was passed, or a new one.
-
-    The caller goes on with it on the current stream, so the allocator is told: the memory is
-    not handed out again before that stream is done with it either."""
-    if t is not None:
-        return t
-    t = _empty(dtype, shape, like, stream)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream(like.device))
-    return t
 
 
 def _workspace(ws, nbytes, like, stream):

@@ -75,3 +75,33 @@ def _check(call):
                                   "swiglu_ckpt8_bwd", "layernorm", "layernorm_bwd"])
 def test_training_outputs_are_not_memory_in_use(name):
     _check(_training_calls()[name])
+
+
+def _layer_calls():
+    T, d, E, k, f = 130, 128, 4, 2, 192
+    x, wg = _randn((T, d), 1), _randn((E, d), 2, d ** -0.5, torch.float32)
+    w1, w3, w2 = _randn((E, f, d), 3, d ** -0.5), _randn((E, f, d), 4, d ** -0.5), _randn((E, d, f), 5, f ** -0.5)
+    ids, w, _ = mk.mk_moe_route(x, wg, None, k)
+    disp = mk.mk_moe_dispatch(x, ids, w, E)
+    off, rows, slot, weight = (disp[n] for n in ("expert_offsets", "x_perm", "slot_row", "row_weight"))
+    counts = torch.tensor([[50, 0], [30, 50]], dtype=torch.int32, device=DEV)  # of x's 130 rows
+    ws = mk.alloc_workspace(T, d, E, k, f)
+    mk.mk_moe_layer(x, wg, None, w1, w3, w2, k, ws=ws)
+    torch.cuda.synchronize()
+    return {
+        "route": lambda **s: mk.mk_moe_route(x, wg, None, k, **s),
+        "dispatch": lambda **s: mk.mk_moe_dispatch(x, ids, w, E, **s),
+        "expert_ffn": lambda **s: mk.mk_moe_expert_ffn(rows, off, weight, w1, w3, w2, **s),
+        "grouped_gemm": lambda **s: mk.mk_moe_grouped_gemm(rows, off, w1, **s),
+        "dispatch_gemm": lambda **s: mk.mk_moe_dispatch_gemm(x, wg, None, w1, k, **s),
+        "combine": lambda **s: mk.mk_moe_combine(rows, slot, **s),
+        "layer": lambda **s: mk.mk_moe_layer(x, wg, None, w1, w3, w2, k, **s),
+        "layer_routing": lambda **s: mk.mk_moe_layer_routing(ws, T, d, E, k, f, **s),
+        "ep_regroup": lambda **s: mk.mk_moe_ep_regroup(x, counts, True, **s),
+    }
+
+
+@pytest.mark.parametrize("name", ["route", "dispatch", "expert_ffn", "grouped_gemm", "dispatch_gemm", "combine",
+                                  "layer", "layer_routing", "ep_regroup"])
+def test_layer_outputs_are_not_memory_in_use(name):
+    _check(_layer_calls()[name])
