@@ -38,6 +38,7 @@
 // on fixed latencies, 1.16 on shared memory and shuffles, 0.94 at the row's
 // barrier and 0.60 on global memory.
 #include <algorithm>
+#include <atomic>
 #include <numeric>
 
 #include "mk_device.cuh"
@@ -637,11 +638,21 @@ int grid_blocks(const RowShape& s, int64_t rows, int d, int most) {
     return std::max(unit, most / unit * unit);
 }
 
-template <typename F>
-cudaError_t allow_smem(F fn, size_t bytes) {
-    return bytes <= 40 * 1024 ? cudaSuccess  // 48 KB with the static part need no leave
-                              : cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(bytes));
+// Leave for `fn`'s launches to use up to kSmSmem of shared memory, once per device.
+// The attribute is the function's, not the launch's: set to each call's own need, a
+// call in another thread could lower it between this call's leave and its launch.
+template <auto fn>
+cudaError_t allow_smem() {
+    static std::atomic<int> configured[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+        err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmSmem));
+        if (err != cudaSuccess) return err;
+        if (dev < 64) configured[dev].store(1, std::memory_order_release);
+    }
+    return cudaSuccess;
 }
 
 struct NormArgs {
@@ -661,11 +672,11 @@ struct NormArgs {
     int blocks;  // out: partial rows written
 };
 
-template <typename T, int NV>
+template <typename T, int NV, bool kAligned>
 cudaError_t launch_fwd(const NormArgs& a, RowShape r) {
     const Ring q = ring_shape(r, RingPart<T, NV>::kWords);  // 16384 fp32 values fit three times
-    auto fn = a.d % 8 == 0 ? layernorm_kernel<T, NV, true> : layernorm_kernel<T, NV, false>;
-    const cudaError_t err = allow_smem(fn, q.bytes);
+    constexpr auto fn = layernorm_kernel<T, NV, kAligned>;
+    const cudaError_t err = allow_smem<fn>();
     if (err != cudaSuccess) return err;
     fn<<<grid_blocks(r, a.rows, a.d, q.blocks * device_sm_count()), r.threads(), q.bytes, a.s>>>(
         static_cast<const T*>(a.x), a.gamma, a.beta, a.rows, a.d, a.eps, r.warps, static_cast<bf16*>(a.y), a.mean,
@@ -673,18 +684,20 @@ cudaError_t launch_fwd(const NormArgs& a, RowShape r) {
     return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool kAligned>
 cudaError_t run_fwd(const NormArgs& a) {
     const RowShape r = row_shape(a.rows, a.d, true);
-    return r.nv == 1 ? launch_fwd<T, 1>(a, r) : r.nv == 2 ? launch_fwd<T, 2>(a, r) : launch_fwd<T, 4>(a, r);
+    return r.nv == 1   ? launch_fwd<T, 1, kAligned>(a, r)
+           : r.nv == 2 ? launch_fwd<T, 2, kAligned>(a, r)
+                       : launch_fwd<T, 4, kAligned>(a, r);
 }
 
-template <typename T, int NV, int STAGES>
+template <typename T, int NV, bool kAligned, int STAGES>
 cudaError_t launch_bwd(NormArgs& a, const RowShape& r, const Ring& q) {
     const size_t smem = std::max(q.bytes, 2 * sizeof(float) * static_cast<size_t>(a.d) * r.rows);
     a.blocks = grid_blocks(r, a.rows, a.d, std::min(q.blocks * device_sm_count(), kMaxBwdBlocks));
-    auto fn = a.d % 8 == 0 ? layernorm_bwd_kernel<T, NV, true, STAGES> : layernorm_bwd_kernel<T, NV, false, STAGES>;
-    const cudaError_t err = allow_smem(fn, smem);
+    constexpr auto fn = layernorm_bwd_kernel<T, NV, kAligned, STAGES>;
+    const cudaError_t err = allow_smem<fn>();
     if (err != cudaSuccess) return err;
     fn<<<a.blocks, r.threads(), smem, a.s>>>(static_cast<const bf16*>(a.dy), static_cast<const T*>(a.x), a.gamma,
                                              a.mean, a.rstd, static_cast<const T*>(a.dres), a.rows, a.d, r.warps,
@@ -692,19 +705,29 @@ cudaError_t launch_bwd(NormArgs& a, const RowShape& r, const Ring& q) {
     return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool kAligned>
 cudaError_t run_bwd(NormArgs& a) {
     RowShape r = row_shape(a.rows, a.d, false);
     const int xs = a.dres != nullptr ? 2 : 1;
     const Ring q = ring_shape(r, r.nv * (RingPart<T, 1>::kWords * xs + RingPart<bf16, 1>::kWords));
-    if (q.stages == 1) return launch_bwd<T, 4, 1>(a, r, q);  // fp32 rows of over 11000 values with dres
+    if (q.stages == 1) return launch_bwd<T, 4, kAligned, 1>(a, r, q);  // fp32 rows of over 11000 values with dres
     if (q.stages == 2)
-        return r.nv == 1   ? launch_bwd<T, 1, 2>(a, r, q)
-               : r.nv == 2 ? launch_bwd<T, 2, 2>(a, r, q)
-                           : launch_bwd<T, 4, 2>(a, r, q);
-    return r.nv == 1   ? launch_bwd<T, 1, 3>(a, r, q)
-           : r.nv == 2 ? launch_bwd<T, 2, 3>(a, r, q)
-                       : launch_bwd<T, 4, 3>(a, r, q);
+        return r.nv == 1   ? launch_bwd<T, 1, kAligned, 2>(a, r, q)
+               : r.nv == 2 ? launch_bwd<T, 2, kAligned, 2>(a, r, q)
+                           : launch_bwd<T, 4, kAligned, 2>(a, r, q);
+    return r.nv == 1   ? launch_bwd<T, 1, kAligned, 3>(a, r, q)
+           : r.nv == 2 ? launch_bwd<T, 2, kAligned, 3>(a, r, q)
+                       : launch_bwd<T, 4, kAligned, 3>(a, r, q);
+}
+
+// The kernels for x's type and for rows that start a 16-byte word or not.
+cudaError_t run(NormArgs& a, int x_type, bool forward) {
+    const bool aligned = a.d % 8 == 0;
+    if (x_type == MK_TYPE_FP32)
+        return forward ? (aligned ? run_fwd<float, true>(a) : run_fwd<float, false>(a))
+                       : (aligned ? run_bwd<float, true>(a) : run_bwd<float, false>(a));
+    return forward ? (aligned ? run_fwd<bf16, true>(a) : run_fwd<bf16, false>(a))
+                   : (aligned ? run_bwd<bf16, true>(a) : run_bwd<bf16, false>(a));
 }
 
 mk_status check_norm(int64_t T, int d, int x_type) {
@@ -730,8 +753,7 @@ extern "C" mk_status mk_moe_layernorm(const void* x, int x_type, const float* ga
     NormArgs a{};
     a.x = x, a.gamma = gamma, a.rows = static_cast<int>(T), a.d = d, a.s = static_cast<cudaStream_t>(stream);
     a.beta = beta, a.eps = eps, a.y = y, a.mean = mean, a.rstd = rstd;
-    const cudaError_t err = x_type == MK_TYPE_FP32 ? run_fwd<float>(a) : run_fwd<bf16>(a);
-    return err == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    return run(a, x_type, true) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
 extern "C" size_t mk_moe_layernorm_bwd_workspace_size(int64_t T, int d) {
@@ -767,7 +789,7 @@ extern "C" mk_status mk_moe_layernorm_bwd(const void* dy, const void* x, int x_t
     a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
     a.dy = dy, a.dres = dres, a.dx = dx;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    if ((x_type == MK_TYPE_FP32 ? run_bwd<float>(a) : run_bwd<bf16>(a)) != cudaSuccess) return MK_ERR_CUDA;
+    if (run(a, x_type, false) != cudaSuccess) return MK_ERR_CUDA;
     const LaunchCfg lc(dim3(static_cast<unsigned>((2 * static_cast<int64_t>(d) + 31) / 32)), dim3(256), 0, s, true);
     if (cudaLaunchKernelEx(&lc.cfg, layernorm_bwd_sum_kernel, static_cast<const float*>(a.part), a.blocks, d, dgamma,
                            dbeta) != cudaSuccess)
