@@ -74,6 +74,17 @@ constexpr uint32_t WHALF_BYTES = 2 * WBOX_BYTES;         // 128 columns
 constexpr uint32_t WSTAGE_BYTES = 2 * WHALF_BYTES;       // this CTA's dout and x columns
 constexpr int kWEpiWarps = 8;                            // two per TMEM quarter, half of the columns each
 constexpr uint32_t WSTORE_BYTES = 32 * 128;              // one store of an epilogue warp
+// The other one of an epilogue warp's two store buffers, wherever the pair lies (dynamic
+// shared memory is aligned to 1024 bytes here, not to the pair's size); `both` is the sum
+// of their addresses.
+__host__ __device__ constexpr uint32_t both_bufs(uint32_t first) { return 2 * first + WSTORE_BYTES; }
+__host__ __device__ constexpr uint32_t other_buf(uint32_t buf, uint32_t both) { return both - buf; }
+constexpr bool swaps_at(uint32_t first) {
+    return other_buf(first, both_bufs(first)) == first + WSTORE_BYTES &&
+           other_buf(first + WSTORE_BYTES, both_bufs(first)) == first;
+}
+static_assert(swaps_at(0) && swaps_at(1024) && swaps_at(WSTORE_BYTES) && swaps_at(WSTORE_BYTES + 1024),
+              "the store buffers swap at any base");
 constexpr int kWSchedWarp = 2;
 constexpr int kWEpiWarp0 = 4;  // registers move between warpgroups; warp 3 only fills up the first
 constexpr int WNUM_THREADS = 32 * (kWEpiWarp0 + kWEpiWarps);
@@ -587,6 +598,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
         const int sub = warp & 3;            // TMEM lanes [32 sub, 32 sub + 32) are this warp's
         const int half = (warp - kWEpiWarp0) >> 2;  // and columns [128 half, 128 half + 128)
         uint32_t buf = smem_u32(store_smem + (warp - kWEpiWarp0) * (kBufs * WSTORE_BYTES));
+        const uint32_t bufs = both_bufs(buf);
         SlotCursor cur;
         const uint32_t buf_row = lane * 128 + (lane & 7) * 16;
         uint32_t acc = 0, acc_phase = 0;
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(WNUM_THREADS, 1)
                             tma_store_2d(&tmOut, col0 + c, out_row, buf);
                         bulk_commit();
                     }
-                    if (kBufs == 2) buf ^= WSTORE_BYTES;  // the pair is aligned to its size
+                    if (kBufs == 2) buf = other_buf(buf, bufs);
                 }
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) sum[c + i] = 0.0f;
