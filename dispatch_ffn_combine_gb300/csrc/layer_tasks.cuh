@@ -17,8 +17,8 @@ namespace tasks {
 constexpr int kThreads = 256;
 
 // Top-k of one token by one warp: k rounds of a warp-wide arg-max (larger
-// logit wins, equal logits go to the lower expert id), then the softmax over
-// the chosen k in fp32.
+// logit wins, equal logits go to the lower expert id, NaN ranks as -inf), then the
+// softmax over the chosen k in fp32.
 __device__ __forceinline__ void topk_token(const float* __restrict__ logits, int64_t t, int E, int k,
                                            int32_t* __restrict__ ids, float* __restrict__ w) {
     const int lane = threadIdx.x & 31;
@@ -64,6 +64,7 @@ __device__ __forceinline__ void topk_token(const float* __restrict__ logits, int
 #pragma unroll
         for (int j = 0; j < kMaxTopK; ++j) {
             if (j >= k) break;
+            sel_v[j] = chosen_logit(sel_v[j], logits + t * E + sel_i[j]);
             ex[j] = expf(sel_v[j] - sel_v[0]);
             z += ex[j];
         }

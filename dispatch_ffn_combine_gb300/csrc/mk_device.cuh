@@ -416,10 +416,16 @@ __device__ __forceinline__ bool wait_count_bounded(const uint32_t* p, uint32_t w
 
 // ----------------------------------------------------------------- small numerics
 
-// A logit for an arg-max: NaN ranks below every number.  Comparisons with NaN
+// A logit for an arg-max: NaN ranks as -inf, the lowest.  Comparisons with NaN
 // are false both ways, so lanes holding one would disagree on the winner and a
 // token could be left without k experts.
 __device__ __forceinline__ float rankable(float v) { return v == v ? v : __uint_as_float(0xff800000u); }
+
+// The chosen logit for the softmax, where the arg-max gave `ranked` and the logit
+// lies at `logit`: what ranked as -inf may be NaN, which the weights have to show.
+__device__ __forceinline__ float chosen_logit(float ranked, const float* logit) {
+    return ranked == __uint_as_float(0xff800000u) ? *logit : ranked;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

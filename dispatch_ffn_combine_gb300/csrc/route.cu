@@ -51,8 +51,8 @@ cudaError_t launch_logits_shape(const uint16_t* xb, const float* wg, const float
 }
 
 // One warp per token: k rounds of a warp-wide arg-max (larger logit wins,
-// equal logits go to the lower expert id, NaN ranks last), then the softmax over
-// the chosen k (NaN weights where the logits were NaN or infinite).
+// equal logits go to the lower expert id, NaN ranks as -inf), then the softmax over
+// the chosen k (NaN weights where a chosen logit is NaN or +inf, or all are -inf).
 __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ logits, int64_t T, int E, int k,
                                                    int32_t* __restrict__ ids, float* __restrict__ w,
                                                    int32_t* __restrict__ counts) {
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ log
 #pragma unroll
         for (int j = 0; j < kMaxTopK; ++j) {
             if (j >= k) break;
+            sel_v[j] = chosen_logit(sel_v[j], logits + t * E + sel_i[j]);
             ex[j] = expf(sel_v[j] - sel_v[0]);
             z += ex[j];
         }

@@ -534,6 +534,8 @@ __global__ void __launch_bounds__(kSelThreads) route_select_kernel(
             float ex[kMaxTopK];
             float z = 0.0f;
             for (int j = 0; j < k; ++j) {
+                // a candidate of -inf or NaN fails its check, so the list is every expert's
+                sel_v[j] = chosen_logit(sel_v[j], cval + sel_i[j]);
                 ex[j] = expf(sel_v[j] - sel_v[0]);
                 z += ex[j];
             }

@@ -68,6 +68,50 @@ def test_route_with_a_nan_expert(T, d, E, k):
     assert torch.equal(ids, ids2) and torch.equal(w, w2)
 
 
+# the last takes the tensor-core candidate filter
+@pytest.mark.parametrize("T,d,E,k,good", [(5, 64, 3, 3, 2), (40, 128, 12, 4, 1), (2048, 8192, 256, 8, 3)])
+def test_route_shows_nan_logits_that_are_chosen(T, d, E, k, good):
+    """Fewer numbers than k among a token's logits: NaN ones are chosen, and every weight of the token is NaN, as
+    the softmax over them is.  Experts masked by -inf have the weight 0 and leave the others' as they are."""
+    x, wg = _inputs(T, d, E)
+    keep = torch.arange(0, E, E // good, device=x.device)[:good]
+    drop = torch.ones(E, dtype=torch.bool, device=x.device)
+    drop[keep] = False
+    bad = wg.clone()
+    bad[drop] = float("nan")
+    ids, w, counts = mk.mk_moe_route(x, bad, None, k)
+    _check_valid(ids, counts, E)
+    assert bool(torch.isnan(w).all())
+    assert torch.equal(ids[:, :good].sort(1).values, keep.to(torch.int32).expand(T, good))
+    bias = torch.zeros(E, device=x.device)
+    bias[drop] = float("-inf")
+    ids, w, counts = mk.mk_moe_route(x, wg, bias, k)
+    _check_valid(ids, counts, E)
+    logits = x.double() @ wg[keep].double().t()
+    want = torch.softmax(logits, 1).sort(1, descending=True).values
+    # logits of size 5 at most, off by d 2^-23 of it, and a few fp32 operations
+    torch.testing.assert_close(w[:, :good].double(), want, rtol=5 * d * 2.0 ** -23 + 1e-5, atol=1e-6)
+    assert not bool(w[:, good:].any())
+    if T * E <= 1 << 21:
+        n_ids, n_w = torch.empty_like(ids), torch.empty_like(w)
+        mk.mk_moe_route_noalloc(x, bad, None, k, n_ids, n_w)
+        assert bool(torch.isnan(n_w).all())
+
+
+@pytest.mark.parametrize("path", [mk.MK_PATH_STEPS, mk.MK_PATH_TILES, mk.MK_PATH_FUSED])
+def test_layer_shows_nan_logits_that_are_chosen(path):
+    """One gate row of numbers and k > 1: the NaN experts that each token also gets show in its output."""
+    cfg = CONFIGS["ragged"]
+    assert cfg.k > 1
+    inp = make_inputs(cfg, seed=0, device="cuda")
+    wg = inp["wg"].clone()
+    wg[1:] = float("nan")
+    ws = mk.alloc_workspace(cfg.T, cfg.d, cfg.E, cfg.k, cfg.f)
+    y = mk.mk_moe_layer(inp["x"], wg, inp["bias"], inp["w1"], inp["w3"], inp["w2"], cfg.k, ws=ws, path=path)
+    assert mk.mk_moe_last_device_error(ws)[0] == mk.MK_OK
+    assert bool(torch.isnan(y).all())
+
+
 @pytest.mark.parametrize("path", [mk.MK_PATH_STEPS, mk.MK_PATH_TILES, mk.MK_PATH_FUSED])
 def test_layer_with_a_nan_token(path):
     cfg = CONFIGS["ragged"]
