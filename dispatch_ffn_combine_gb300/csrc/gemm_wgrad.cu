@@ -42,7 +42,9 @@
 //   store       the epilogue warps pass 32 x 128 bytes at a time through
 //               swizzled shared memory to TMA stores (adding: TMA reductions
 //               in L2, each element once per call, so the result does not
-//               depend on timing).  An expert without rows gets zeros.
+//               depend on timing; such additions may take subnormal values as
+//               zero, though a GB300 was seen to keep them).  An expert without
+//               rows gets zeros.
 //
 // Bound by the tensor cores where experts have many rows, by storing dW where they
 // have few.  Measured, of the measured burst bf16 rate (R) or copy rate (C): 131072

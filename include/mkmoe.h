@@ -443,7 +443,8 @@ MK_API mk_status mk_moe_grouped_dgrad(const void* dout, const int32_t* expert_of
  *   dout bf16 [S, n]; x_perm bf16 [S, d]; expert_offsets as above
  *   dw   [E, n, d] (out): dw_type MK_TYPE_FP32 or MK_TYPE_BF16.  accumulate != 0
  *        (fp32 only) adds to dw; otherwise dw is overwritten, with zeros for an
- *        expert without rows (and for all of them when S == 0).
+ *        expert without rows (and for all of them when S == 0).  Adding may take
+ *        what is below 2^-126 in magnitude (dw, a sum or the result) as zero.
  *   ws: at least 256 bytes.  With mk_moe_grouped_wgrad_workspace_size() bytes
  *        the sums of few, long experts are split over the GPU and joined in row
  *        order (the same sums, rounded in another order).
