@@ -41,3 +41,48 @@ def test_wgrad_adds_next_to_the_normal_range(counts):
     for e, c in enumerate(counts):
         if c == 0:
             assert torch.equal(dw[e], before[e])
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("pieces", [False, True])
+def test_wgrad_long_sum_error_in_norm(pieces, accumulate):
+    """20000 rows of one expert: whole, in 27 chunks of 768 rows whose sums join in registers (the least workspace),
+    and in pieces that a second kernel joins.
+
+    A chunk is 48 MMA steps, each truncating by at most 2^-23 of the running sum, which is 2/3 of the chunk's
+    sum on average (it grows with the root of the steps): 48 * 2^-23 * 2/3 = 3.8e-6 of the chunk's sum at most.
+    The chunks' sums and their errors have random signs and grow alike, and the additions between them are
+    rounded to nearest (2^-25 each on average): 4e-6 in norm.  One long truncated sum is at 1e-5 and more."""
+    S, n, d = 20000, 256, 256
+    g = torch.Generator().manual_seed(3)
+    do, x = (torch.randn((S, c), generator=g).to(BF).to(DEV) for c in (n, d))
+    off = _offsets([S])
+    size = mk.load_library().mk_moe_grouped_wgrad_workspace_size(S, d, 1, n)
+    assert size > 256
+    ws = torch.empty(size if pieces else 256, dtype=torch.uint8, device=DEV)
+    before = torch.randn((1, n, d), generator=g).to(DEV)
+    dw = before.clone()
+    mk.mk_moe_grouped_wgrad(do, off, x, dw=dw, accumulate=accumulate, ws=ws)
+    want = ref.wgrad(do, off, x, 1) + (before.to(F64) if accumulate else 0)
+    assert float((dw.to(F64) - want).norm() / want.norm()) <= 4e-6
+
+
+@pytest.mark.parametrize("counts,n,d", [([20000], 64, 64), ([9000, 0, 3001, 1], 256, 192), ([511, 13000], 64, 256),
+                                        ([767, 769, 1536, 0, 1, 2305], 320, 192)])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.float32, False), (torch.float32, True), (BF, False)])
+def test_wgrad_integer_sums_are_exact(counts, n, d, dtype, accumulate):
+    """Operands of -2 to 2: every sum stays below 2^24 and is exact in fp32, in any order, so that a row that is lost
+    or counted twice shows; whole and in pieces."""
+    S, E = sum(counts), len(counts)
+    assert 4 * max(counts) + 100 < 1 << 24
+    off = _offsets(counts)
+    g = torch.Generator().manual_seed(S)
+    do, x = (torch.randint(-2, 3, (S, c), generator=g).to(BF).to(DEV) for c in (n, d))
+    before = torch.randint(-100, 101, (E, n, d), generator=g).to(dtype).to(DEV)
+    want = ref.wgrad(do, off, x, E) + (before.to(F64) if accumulate else 0)
+    for nbytes in {256, max(256, mk.load_library().mk_moe_grouped_wgrad_workspace_size(S, d, E, n))}:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+        dw = before.clone()
+        mk.mk_moe_grouped_wgrad(do, off, x, dw=dw, accumulate=accumulate, ws=ws)
+        assert mk.mk_moe_last_device_error(ws)[0] == mk.MK_OK
+        assert torch.equal(dw, want.to(dtype))
