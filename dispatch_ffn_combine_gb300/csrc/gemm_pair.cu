@@ -31,13 +31,14 @@
 //               transposed copy; activations, tiles, swap tiles, schedule and
 //               epilogue are gemm2's.  With two pairs of operands (gate and up)
 //               the k-blocks of the second follow those of the first into the
-//               same accumulator: one pass over dx instead of two.  Measured:
-//               131072 skewed rows over 64 experts of 4096 x 1536 891-902 us
-//               (0.93 of the measured burst bf16 rate), 16384 rows over 32, two
-//               of 1408 x 2048, 130 us (0.74; its tiles come out uneven over the
-//               SMs, and claiming one or two ahead instead of three changes
-//               nothing), 8191 rows over 256 of 1408 x 2048 232 us (0.98 of the
-//               copy rate).
+//               same accumulator: one pass over dx instead of two.  Measured, 20
+//               calls in a row after a rest, and for 3 s without one (the power
+//               cap's clock): 131072 skewed rows over 64 experts of 4096 x 1536
+//               892 us (0.94 of the measured burst bf16 rate) and 1063 (0.89 of
+//               the sustained one), 16384 rows over 32, two of 1408 x 2048, 132
+//               (0.73) and 145 (0.75; claiming one or two tiles ahead instead of
+//               three changes nothing); 8191 rows over 256 of 1408 x 2048, after
+//               a rest, 229 (1.0 of the copy rate).
 //   why         per SM and k-block, 32 KB of operands cross L2 and shared
 //               memory instead of 48 KB (B is split, not duplicated), so seven
 //               stages (3584 cycles of MMA work) fit instead of four.

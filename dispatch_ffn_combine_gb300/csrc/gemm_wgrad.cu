@@ -47,12 +47,14 @@
 //               rows gets zeros.
 //
 // Bound by the tensor cores where experts have many rows, by storing dW where they
-// have few.  Measured, of the measured burst bf16 rate (R) or copy rate (C): 131072
-// skewed rows over 64 experts of 1536 x 4096 fp32 980 us (0.86 R), adding 1210
-// (0.69 R: the additions read the gradient too, 1.6 GB); 16384 rows over
-// 32 of 1408 x 2048 fp32 105 us (0.68 C), adding 141 (0.90 C), bf16 88 (0.55 R);
-// 8191 rows over 256 of them, bf16 302 us (0.76 C; the MMA warp and the epilogue
-// wait on each other for accumulators, not for stores), fp32 adding 880 (1.01 C).
+// have few.  Measured, 20 calls in a row after a rest, of the measured burst bf16
+// rate (R) or copy rate (C): 131072 skewed rows over 64 experts of 1536 x 4096 fp32
+// 980 us (0.86 R), adding 1127 (0.75 R: the additions read the gradient too, 1.6 GB;
+// for 3 s without a rest, at the power cap's clock, 1131 and 1208); 16384 rows over
+// 32 of 1408 x 2048 fp32 105 to 111 us (0.68 to 0.65 C; what holds it was not
+// measured), adding 141 (0.90 C), bf16 88 to 94 (0.55 to 0.51 R; nor here); 8191
+// rows over 256 of them, bf16 303 us (0.76 C; the MMA warp and the epilogue wait on
+// each other for accumulators, not for stores), fp32 adding 880 (1.01 C).
 //
 // Every wait is bounded, as in the other pair kernels.
 #include <algorithm>

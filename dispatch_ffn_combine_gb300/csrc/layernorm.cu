@@ -31,7 +31,7 @@
 //
 // Measured, and the share of the measured copy rate: 32768 x 7168 bf16 forward
 // 146 us (0.96), backward 249 us (0.84); 16384 x 4096 fp32 forward 66 us (0.91),
-// backward with dres 146 us (0.96); 16384 x 4095 bf16 70 us (0.57) and 123 us
+// backward with dres 146 us (0.96); 16384 x 4095 bf16 67 us (0.59) and 123 us
 // (0.49).  At 16384 x 7168 bf16 the backward kernel executes 20.7 instructions per
 // value (6.6 integer, 6.1 fp32) on the 14 warps of its 126 registers, with the
 // issue slots 50 % busy and DRAM at 67 %; per instruction a warp waits 1.25 cycles
@@ -149,8 +149,7 @@ __device__ __forceinline__ uint32_t after(uint32_t addr) {
 // then the same tree over the warps' sums (a chain over up to 16 warps took
 // longer than all the rest of a row).  The group alone meets at its named
 // barrier.  There are two buffers, used in turn: a buffer is written again only
-// after the barrier of the sum between.  (Two values in the halves of one tree
-// took fewer instructions and longer: a row waits for the chain of shuffles.)
+// after the barrier of the sum between.
 template <int N>
 struct GroupSum {
     static constexpr uint32_t kBuffer = kMaxWarps * N * 4;

@@ -46,7 +46,10 @@ class MoEBlock:
 
 
 def forward(block: MoEBlock, x: torch.Tensor):
-    """x [T, d] (bf16 or fp32 residual stream) -> (out like x, what `backward` needs)."""
+    """x [T, d] (bf16 or fp32 residual stream) -> (out like x, what `backward` needs).
+
+    The layer works on bf16 whatever x is: the norm's output, gate, up, h, each expert's output and their
+    sum y are rounded to it, as in the forward layer; the residual sum is in x's type."""
     E = block.w1.shape[0]
     n, mean, rstd = mk_moe_layernorm(x, block.gamma, block.beta, block.eps)
     ids, w, _ = mk_moe_route(n, block.wg, block.bias, block.k)
@@ -66,7 +69,9 @@ def _gate_backward(block: MoEBlock, saved: dict, drow_weight: torch.Tensor, n: t
 
     The weights are a softmax over the chosen k, so with dw[t, j] the gradient of token t's j-th weight
     dl[t, j] = w[t, j] (dw[t, j] - sum_i w[t, i] dw[t, i]) is that of its chosen logits; the others have none.
-    T x E values in fp32: small beside the experts, left to torch."""
+    The sums over d and T are in fp32 and left to torch.  Measured, of a whole forward and backward pass: 5.2 of
+    59 ms for 32768 tokens of 7168 values and 256 experts of width 2048, 0.14 of 1.4 ms for the mid workload, 0.25 of
+    1.0 ms for tiny (launches)."""
     w = saved["w"]
     dw = drow_weight[saved["slot_row"].long()]
     dl = w * (dw - (w * dw).sum(1, keepdim=True))
@@ -78,7 +83,13 @@ def _gate_backward(block: MoEBlock, saved: dict, drow_weight: torch.Tensor, n: t
 
 
 def backward(block: MoEBlock, saved: dict, dout: torch.Tensor, grads: dict) -> torch.Tensor:
-    """dout [T, d] in x's type -> dx; adds the weights' gradients to `grads` (see zero_grads)."""
+    """dout [T, d] in x's type -> dx; adds the weights' gradients to `grads` (see zero_grads).
+
+    What has fewer bits than fp32, each for the types that the tensor cores and the kernels take, and for half the
+    bytes: dout as it is dispatched (the residual's part of dx keeps x's type), dh, dgate, dup and the weighted
+    activation, each expert's share of the norm output's gradient, their sum, and that sum with the gate's part,
+    all bf16.  w1's and w3's gradients multiply the tokens, w2's the activation, as their 8-bit copies hold them;
+    those copies are the larger error by far (2.6 % rms of a value against 0.2 %).  All sums are fp32."""
     off, slot_row = saved["offsets"], saved["slot_row"]
     x = saved["x"]
     # combine's gradient is the dispatch of dout; the routing weight is applied in SwiGLU's backward pass
