@@ -7,6 +7,7 @@
 #include <atomic>
 #include <numeric>
 
+#include "f32x2.cuh"
 #include "mk_device.cuh"
 #include "mk_internal.h"
 
@@ -16,37 +17,6 @@ namespace norm_rows {
 constexpr int kMaxD = 16384;  // 16 warps of 4 vectors; 8 less where a row's first word may start before it
 constexpr int kMaxWarps = 16;    // per block and per row
 constexpr int kMaxBwdBlocks = 304;  // partial rows of a backward pass
-
-// ---------------------------------------------------------------- packed fp32 pairs
-
-// Two fp32 values in one 64-bit register, the operands of the f32x2 instructions.
-struct f2 {
-    uint64_t v;
-    __device__ __forceinline__ f2() {}
-    __device__ __forceinline__ f2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-    __device__ __forceinline__ float x() const {
-        return __uint_as_float(static_cast<uint32_t>(v));
-    }
-    __device__ __forceinline__ float y() const {
-        return __uint_as_float(static_cast<uint32_t>(v >> 32));
-    }
-};
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ f2 both(float v) { return f2(v, v); }
 
 // ---------------------------------------------------------------- eight values
 

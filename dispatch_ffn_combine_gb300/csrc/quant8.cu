@@ -3,7 +3,7 @@
 // 128 values (weights: 128 x 128).
 //
 // All three are bound by HBM: each value is read once and each code written once (262144 x
-// 2048: rows 265 us, 0.90 of the copy rate, SwiGLU 385, 1.03; weights at 0.93 to 0.96).
+// 2048: rows 249 us, 0.96 of the copy rate, SwiGLU 379, 1.05; weights at 0.90).
 //
 // Rows: eight lanes hold a block, 16 values each (two 16-byte loads per tensor, one
 // 16-byte store), so a warp has four blocks at a time: of one row, or of two or four
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) quant8_rows_kernel(const bf16*
     const bf16* xr = x + (live ? row : 0) * ld;
     const bf16* ur = kSwiGLU ? up + (live ? row : 0) * ld : nullptr;
     int b = blockIdx.y * steps * per_row + group % per_row;
-#pragma unroll 2
+#pragma unroll 1
     for (int s = 0; s < steps; ++s, b += per_row) {
         const int col = b * kScaleBlock + in_block * kLaneVals;
         const bool in = live && col < c;  // c is a multiple of 64: all 16 values or none
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) quant8_rows_kernel(const bf16*
 
 constexpr int kWThreads = 256;
 
-__global__ void __launch_bounds__(kWThreads, 4) quant8_weights_kernel(const bf16* __restrict__ w, int n, int d, int k_blocks,
+__global__ void __launch_bounds__(kWThreads, 3) quant8_weights_kernel(const bf16* __restrict__ w, int n, int d, int k_blocks,
                                                                    int n_blocks, int pitch, uint8_t* __restrict__ codes,
                                                                    float* __restrict__ scales) {
     __shared__ float most[2][kWThreads / 32];
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kWThreads, 4) quant8_weights_kernel(const bf16
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r0 = nb * kScaleBlock + (threadIdx.x >> 3), col = kb * kScaleBlock + (threadIdx.x & 7) * 16;
     const int64_t base = static_cast<int64_t>(e) * n;
-    // Rows r0, r0 + 32, ..., kept as bf16: half the registers, four thread blocks per SM instead of two (16 experts of
-    // 4096 x 7168: 408 -> 222 us, 0.93 of the copy rate).
+    // Rows r0, r0 + 32, ..., kept as bf16: half the registers, three thread blocks per SM instead of two (16 experts of
+    // 4096 x 7168: 230 us, 0.90 of the copy rate; with fp32 values held 408, with four blocks, whose 64 registers spill, 240).
     Raw16 raw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

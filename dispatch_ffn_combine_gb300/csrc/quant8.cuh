@@ -2,17 +2,19 @@
 // 8-bit grouped GEMM takes them.
 //
 // A block's scale is amax / 448 (2^-126 at least), amax the largest finite
-// magnitude of the block and 448 the largest e4m3 value; a code is v / scale
-// rounded to nearest even, so a value is off by at most 2^-4 |v|, or half a step
-// of 2^-9 scale where the code is subnormal.  The quotient is taken as v times
-// the rounded reciprocal of the scale: two roundings in fp32, 2^-23 in all, which
-// can move a value across the middle between two codes but adds no more than that
-// to its error.  The bound of 2^-126 keeps the reciprocal finite.  NaN and
-// infinities become e4m3's NaN, so that what went wrong is still seen.
+// magnitude of the block and 448 the largest e4m3 value; a code is the quotient
+// v / scale, rounded to nearest in fp32 and then to nearest even, so a value is off by at
+// most 2^-4 |v|, or half a step of 2^-9 scale where the code is subnormal.  The quotient
+// is v times the reciprocal of the scale, corrected by its remainder (Markstein's
+// division: with the reciprocal rounded to nearest and an exact remainder the corrected
+// quotient is rounded to nearest); the product alone, off by two roundings, gave other
+// codes next to the middle between two.  The bound of 2^-126 keeps the reciprocal finite.
+// NaN and infinities become e4m3's NaN, so that what went wrong is still seen.
 #pragma once
 
 #include <cuda_fp8.h>
 
+#include "f32x2.cuh"
 #include "mk_device.cuh"
 #include "mk_internal.h"
 
@@ -82,16 +84,33 @@ __device__ __forceinline__ float block_scale(float (&f)[N]) {
     return scale_of(m);
 }
 
-// Codes of N values.
-template <int N>
-__device__ __forceinline__ void encode(const float (&f)[N], float scale, uint32_t (&c)[N / 4]) {
-    const float inv = __frcp_rn(scale);
+// Codes of N values.  The smallest blocks' values and scale are raised by 2^64, exactly: the remainders of
+// what is not rounded to zero are normal numbers.
+template <int N, bool kRaised>
+__device__ __forceinline__ void encode_block(const float (&f)[N], float scale, uint32_t (&c)[N / 4]) {
+    if (kRaised) scale *= 0x1p64f;
+    const f2 inv = both(__frcp_rn(scale)), minus = both(-scale);
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        f2 q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f2 v(f[4 * i + 2 * h], f[4 * i + 2 * h + 1]);
+            if (kRaised) v = mul2(v, both(0x1p64f));
+            q[h] = mul2(v, inv);
+            q[h] = fma2(fma2(q[h], minus, v), inv, q[h]);
+        }
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0].x(), q[0].y()), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[1].x(), q[1].y()), __NV_SATFINITE, __NV_E4M3);
         c[i] = lo | (hi << 16);
     }
+}
+template <int N>
+__device__ __forceinline__ void encode(const float (&f)[N], float scale, uint32_t (&c)[N / 4]) {
+    if (scale >= 0x1p-64f)
+        encode_block<N, false>(f, scale, c);
+    else
+        encode_block<N, true>(f, scale, c);
 }
 
 }  // namespace quant8
