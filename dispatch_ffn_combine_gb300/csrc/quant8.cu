@@ -3,16 +3,15 @@
 // 128 values (weights: 128 x 128).
 //
 // All three are bound by HBM: each value is read once and each code written once (262144 x
-// 2048: rows 249 us, 0.96 of the copy rate, SwiGLU 379, 1.05; weights at 0.90).
+// 2048: rows 249 us, 0.96 of the copy rate, SwiGLU 402, 0.99; weights at 0.90).
 //
 // Rows: eight lanes hold a block, 16 values each (two 16-byte loads per tensor, one
 // 16-byte store), so a warp has four blocks at a time: of one row, or of two or four
 // rows that have so few.  Its largest magnitude takes three shuffles.  SwiGLU is
-// rounded once, to the code; its bf16 output is never formed.  The fast exponential and
-// quotient move as few codes from those of exact values as expf and a division do (6 in
-// 5 million; the scale's rounding moves as many) and take 385 us where those take 545 (262144 x 2048),
-// with the quotient alone as a product with the reciprocal 460.  A sigmoid below 2^-126
-// is zero (gates below -87.3).
+// rounded once, to the code; its bf16 output is never formed.  Its exponential is within 6.5 units of
+// 2^-24 for every gate, the rest rounded to nearest.  (With the fast exponential, off by up to
+// 1.2 |g| units of 2^-23 more, and the fast quotient, zero for gates below -87.3, 379 us; with expf and
+// a division 510, with expf and the corrected quotient 480.)
 //
 // Weights: a thread block per 128 x 128 values, held in registers between the pass
 // for the largest magnitude and the one for the codes.
@@ -44,6 +43,55 @@ __device__ __forceinline__ void unpack(const Raw16& r, float (&f)[16]) {
 }
 __device__ __forceinline__ void load16(const bf16* p, float (&f)[16]) { unpack(load_raw(p), f); }
 
+// silu(g) u = g / (1 + exp(-g)) u in fp32 for a bf16 g.  exp(-g) = 2^(-g a) exp(-g b) with a the 16 bits nearest to
+// log2 e, so that g a is exact, and b = 1 - a ln 2; g b is below 2^-11, so 1 - g b stands for the second factor (2^-23).
+// The quotient is the product with the reciprocal, corrected as in quant8::encode.
+constexpr float kLog2E16 = 47274.0f / 32768.0f, kLog2ERest = 4.888495e-6f;
+constexpr float kLeastGate = -87.0f;  // 1 + exp(87) is below 2^126: the reciprocal is a normal number
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+__device__ __forceinline__ float least(const Raw16& r) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    __nv_bfloat162 m = reinterpret_cast<const __nv_bfloat162&>(w[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmin2(m, reinterpret_cast<const __nv_bfloat162&>(w[i]));
+    return __bfloat162float(__hmin(m.x, m.y));
+}
+// silu(g) for g < kLeastGate, where 1 is no part of the sum: g exp(g), the exponential raised by 2^64 until the product
+// is a normal number.  Zero where exp(-g) is past fp32 (of bf16 gates those from -89 down).
+__device__ __forceinline__ float silu_low(float g) {
+    const float e = ex2_approx(fmaf(g, kLog2E16, 64.0f));
+    return g > -88.75f ? g * fmaf(e, g * kLog2ERest, e) * 0x1p-64f : g * 0.0f;
+}
+__device__ __forceinline__ void swiglu(const Raw16& gate, const Raw16& up, float (&f)[16]) {
+    float u[16];
+    unpack(gate, f);
+    unpack(up, u);
+    const bool low = least(gate) < kLeastGate;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const f2 g(f[2 * i], f[2 * i + 1]);
+        const f2 t = mul2(g, both(-kLog2E16)), rest = mul2(g, both(-kLog2ERest));
+        f2 e(ex2_approx(t.x()), ex2_approx(t.y()));
+        e = fma2(e, rest, e);
+        const f2 d = add2(e, both(1.0f)), minus = fma2(e, both(-1.0f), both(-1.0f));
+        const f2 y(rcp_approx(d.x()), rcp_approx(d.y()));
+        f2 q = mul2(g, y);
+        q = fma2(fma2(q, minus, g), y, q);
+        if (low) q = f2(g.x() < kLeastGate ? silu_low(g.x()) : q.x(), g.y() < kLeastGate ? silu_low(g.y()) : q.y());
+        q = mul2(q, f2(u[2 * i], u[2 * i + 1]));
+        f[2 * i] = q.x(), f[2 * i + 1] = q.y();
+    }
+}
+
 // x (kSwiGLU: gate) and up with row strides ld; a warp takes rows of 1 << row_shift
 // per step and blockIdx.y's `steps` steps of blocks.
 template <bool kSwiGLU>
@@ -66,13 +114,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) quant8_rows_kernel(const bf16*
         const bool in = live && col < c;  // c is a multiple of 64: all 16 values or none
         float f[kLaneVals];
         if (in) {
-            load16(xr + col, f);
-            if constexpr (kSwiGLU) {
-                float u[kLaneVals];
-                load16(ur + col, u);
-#pragma unroll
-                for (int i = 0; i < kLaneVals; ++i) f[i] = __fdividef(f[i], 1.0f + __expf(-f[i])) * u[i];
-            }
+            if constexpr (kSwiGLU)
+                swiglu(load_raw(xr + col), load_raw(ur + col), f);
+            else
+                load16(xr + col, f);
         } else {
 #pragma unroll
             for (int i = 0; i < kLaneVals; ++i) f[i] = 0.0f;

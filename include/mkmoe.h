@@ -592,7 +592,7 @@ MK_API int mk_moe_scale_pitch(int c);
 
 /* Rows of bf16 values in that form: a block's scale is max(amax / 448, 2^-126),
  * amax its largest finite magnitude and 448 the largest e4m3 value; codes round
- * the quotient to nearest even; NaN and infinities become NaN.
+ * the fp32 quotient to nearest even; NaN and infinities become NaN.
  *   x bf16 [S, c] with rows ld values apart (ld >= c, a multiple of 8)
  *   codes uint8 [S, c] (out); scales fp32 [S, pitch(c)] (out)
  * Limits: c a multiple of 64, c < 2^30, S < 2^31, ld < 2^31, S * ld < 2^40. */
@@ -604,8 +604,9 @@ MK_API mk_status mk_moe_quant8_rows(const void* x, int64_t ld, int64_t S, int c,
  * Limits as for mk_moe_grouped_gemm's weights. */
 MK_API mk_status mk_moe_quant8_weights(const void* w, int E, int n, int d, uint8_t* codes, float* scales, void* stream);
 
-/* SwiGLU between two 8-bit products: silu(gate) * up in that form, rounded once (a
- * sigmoid below 2^-126 is zero).
+/* SwiGLU between two 8-bit products: silu(gate) * up in that form, worked out in fp32 as
+ * gate / (1 + exp(-gate)) * up (zero where the exponential is past fp32, of bf16 gates those
+ * from -89 down) and rounded once.
  *   gate, up bf16 [S, f] with rows ld values apart (the halves of one product's
  *   output: ld = 2 f); codes uint8 [S, f] (out); scales fp32 [S, pitch(f)] (out)
  * Limits as for mk_moe_quant8_rows. */

@@ -78,6 +78,57 @@ def _nearest(codes, scales, v, slack):
     return int((off > step / 2).sum())
 
 
+# SwiGLU in fp32 for bf16 gates, in units of 2^-24 of the value: the exponential 4 (ex2's 2^-22), 1.5 for the two factors
+# it is the product of (the second, 1 - g b, leaves out (g b)^2 / 2 < 2^-23.4) and 1 for their product's rounding; the sum
+# with 1, the quotient and the product with up 1 each: 9.5.  The quotient by the scale is one more, and so is the scale.
+SWIGLU = 10.51 * 2.0 ** -24
+
+
+def _check_swiglu(gate, up, codes, scales):
+    gate, up = gate.to(F64), up.to(F64)
+    v = gate * torch.special.expit(gate) * up
+    amax = v.unflatten(1, (-1, 128)).abs().amax(2)
+    s = scales[:, :amax.shape[1]].to(F64)
+    assert bool(((s - amax / 448).abs() <= SWIGLU * amax / 448).all())
+    _nearest(codes, scales[:, :amax.shape[1]], v, SWIGLU)
+
+
+@pytest.mark.parametrize("spread", [1.0, 6.0, 20.0])
+def test_swiglu8_is_the_fp32_form(spread):
+    S, f = 16384, 2048
+    g = torch.Generator(DEV).manual_seed(3)
+    gate = (torch.randn((S, f), generator=g, device=DEV) * spread).to(BF)
+    up = torch.randn((S, f), generator=g, device=DEV).to(BF)
+    codes, scales = mk.mk_moe_swiglu8(gate, up)
+    for a in range(0, S, 4096):
+        _check_swiglu(gate[a:a + 4096], up[a:a + 4096], codes[a:a + 4096], scales[a:a + 4096])
+
+
+def test_swiglu8_of_every_gate():
+    """All finite bf16 gates above -88.7 (below, exp(-g) is past fp32 and the form is zero), each beside ups that bring
+    its product to one size, so that the codes of a block differ by the gates' errors."""
+    bits = torch.arange(1 << 16, device=DEV, dtype=torch.int32)
+    gate = bits.to(torch.int16).view(BF)
+    gate = gate[torch.isfinite(gate) & (gate > -88.7) & (gate != 0)]
+    silu = gate.to(F64) * torch.special.expit(gate.to(F64))
+    gate, silu = gate[silu.abs() >= 2.0 ** -124], silu[silu.abs() >= 2.0 ** -124]
+    for factor in (1.0, 1.3, 1.7):
+        up = (factor / silu).to(F32).to(BF)
+        ok = torch.isfinite(up) & (up.abs() >= 2.0 ** -126)
+        n = int(ok.sum()) // 128 * 128
+        a, b = gate[ok][:n].view(-1, 128), up[ok][:n].view(-1, 128)
+        _check_swiglu(a, b, *mk.mk_moe_swiglu8(a, b))
+
+
+def test_swiglu8_of_gates_whose_sigmoid_is_subnormal():
+    """exp(-g) is finite down to g = -88.72, so the fp32 form has a value there; with ups of 2^120 it counts."""
+    gate = torch.tensor([-80.0, -86.5, -87.0, -87.5, -88.0, -88.5] * 64, device=DEV).to(BF).view(3, 128)
+    up = torch.full_like(gate, 2.0 ** 120)
+    up[1] = 2.0 ** 126
+    up[2, ::2] = -(2.0 ** 125)
+    _check_swiglu(gate, up, *mk.mk_moe_swiglu8(gate, up))
+
+
 @pytest.mark.parametrize("x_type", [BF, F32])
 def test_norm_codes_are_the_fp32_quotients(x_type):
     """y = (h rstd) gamma in fp32 with the rstd that the call gives: two roundings, and one of the quotient."""
