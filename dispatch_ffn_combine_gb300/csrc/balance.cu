@@ -53,6 +53,12 @@ struct Seqs {
     const int32_t* offsets;  // [B + 1] or null: one sequence of all T tokens
     int B;
     int64_t T;
+    // Whether sequence i's bounds are out of order or outside the tokens, or the first one does not start at 0.
+    __device__ __forceinline__ bool bad(int i) const {
+        if (offsets == nullptr) return false;
+        const int32_t a = __ldg(offsets + i), b = __ldg(offsets + i + 1);
+        return a < 0 || b < a || b > T || (i == 0 && a != 0);
+    }
     // Clamped to the tokens, so that no offset leads outside the tensors.
     __device__ __forceinline__ int64_t at(int s) const {
         if (offsets == nullptr) return s == 0 ? 0 : T;
@@ -60,24 +66,28 @@ struct Seqs {
     }
 };
 
-// The first sequence that ends behind token t (B: none), and how many are not empty.  All threads of the block.
+// The first sequence that ends behind token t (B: none), how many are not empty, and whether any has bad bounds.  All
+// threads of the block.
 struct Place {
     int seq, filled;
+    bool bad;
 };
 __device__ __forceinline__ Place find_place(const Seqs& seqs, int64_t t, uint32_t (&s_part)[kWarps]) {
     static_assert(kMaxSeqs < 1 << 16, "two counts in a word");
     uint32_t n = 0;
+    bool bad = false;
     for (int i = threadIdx.x; i < seqs.B; i += kThreads) {
         const int64_t end = seqs.at(i + 1);
         n += (end <= t ? 0x10000u : 0u) + (end > seqs.at(i) ? 1u : 0u);
+        bad |= seqs.bad(i);
     }
     n = __reduce_add_sync(0xffffffffu, n);
     if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = n;
-    __syncthreads();
+    bad = __syncthreads_or(bad ? 1 : 0) != 0;
     n = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) n += s_part[i];
-    return {static_cast<int>(n >> 16), static_cast<int>(n & 0xffffu)};
+    return {static_cast<int>(n >> 16), static_cast<int>(n & 0xffffu), bad};
 }
 
 // A lane's VALS of a token's E logits.  kVec: E is a multiple of four, loaded 16 bytes at a time.
@@ -273,10 +283,7 @@ __global__ void __launch_bounds__(32 * kMaxSlices) balance_sum_kernel(const Loss
     const int e = blockIdx.x * 32 + lane;
     const int64_t t0 = seqs.at(s), n = max(seqs.at(s + 1) - t0, static_cast<int64_t>(0));
     pdl_wait();
-    if (threadIdx.x == 0 && blockIdx.x == 0 && seqs.offsets != nullptr) {
-        const int32_t a = seqs.offsets[s], b = seqs.offsets[s + 1];
-        if (a < 0 || b < a || b > seqs.T || (s == 0 && a != 0)) report_error(status, MK_ERR_BOUNDS, kSiteBalanceOffsets);
-    }
+    if (threadIdx.x == 0 && blockIdx.x == 0 && seqs.bad(s)) report_error(status, MK_ERR_BOUNDS, kSiteBalanceOffsets);
     float p = 0.0f, z = 0.0f;
     int32_t c = 0;
     if (n > 0) {
@@ -379,8 +386,10 @@ __global__ void __launch_bounds__(kThreads, 4) route_bwd_kernel(const RouteBwd a
     const int64_t all = seqs.at(seqs.B);
     const float z_scale = all > 0 ? 2.0f * a.z_coef / static_cast<float>(all) : 0.0f;
     pdl_wait();  // the status was cleared by the kernel before
-    for (int s = place.seq; t < t1; ++s) {
-        const bool in_seq = s < seqs.B;  // else the tokens behind the last sequence: the weights' part only
+    if (place.bad && blockIdx.x == 0 && threadIdx.x == 0) report_error(a.status, MK_ERR_BOUNDS, kSiteBalanceOffsets);
+    for (int s = place.bad ? seqs.B : place.seq; t < t1; ++s) {
+        // else the tokens behind the last sequence, or all of them where the bounds are bad: the weights' part only
+        const bool in_seq = s < seqs.B;
         const int64_t end = in_seq ? min(seqs.at(s + 1), t1) : t1;
         if (end <= t) continue;
         const float n = in_seq ? static_cast<float>(seqs.at(s + 1) - seqs.at(s)) : 1.0f;

@@ -573,7 +573,8 @@ MK_API mk_status mk_moe_balance_loss(const float* logits, const int32_t* topk_id
  *   dlogits fp32 [T, E] (out)
  *   ws: at least 256 bytes.
  * Tokens behind the last sequence get the weights' part only.  An id or row out of
- * range sets MK_ERR_BOUNDS on the device and has no part.  Limits as above. */
+ * range sets MK_ERR_BOUNDS on the device and has no part; bad offsets set it, and
+ * every token gets the weights' part only.  Limits as above. */
 MK_API mk_status mk_moe_route_bwd(const float* logits, const int32_t* topk_ids, const float* topk_w,
                            const float* dweight, const int32_t* slot_row, const int32_t* counts,
                            const int32_t* seq_offsets, int64_t T, int E, int k, int B, float balance_coef,
