@@ -766,6 +766,9 @@ extern "C" mk_status mk_moe_grouped_gemm8(const uint8_t* codes, const float* sca
                                           size_t ws_bytes, void* stream) {
     const mk_status st = check_sizes(S, d, E, 1, n);
     if (st != MK_OK) return st;
+    // Columns are counted in 32 bits, a tile's past the end included; and a tile of 2^28 columns takes 1.2 s, a longer
+    // one more than the bounded waits for its end allow.
+    if (d >= 1 << 28 || n >= 1 << 30) return MK_ERR_UNSUPPORTED;
     if (out_type != MK_TYPE_BF16 && out_type != MK_TYPE_FP32) return MK_ERR_INVALID_ARG;
     if (S == 0) return MK_OK;
     if (!codes || !scales || !expert_offsets || !w_codes || !w_scales || !out) return MK_ERR_INVALID_ARG;

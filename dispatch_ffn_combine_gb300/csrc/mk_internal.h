@@ -305,7 +305,9 @@ bool aligned16(const void* p);
 
 // fp32 scales per row of c values in blocks of 128: a multiple of four, so that rows start on 16 bytes.
 constexpr int kScaleBlock = 128;
-inline int scale_pitch(int c) { return (c + 4 * kScaleBlock - 1) / (4 * kScaleBlock) * 4; }
+inline int scale_pitch(int c) {
+    return static_cast<int>((static_cast<int64_t>(c) + 4 * kScaleBlock - 1) / (4 * kScaleBlock) * 4);  // the sum passes 2^31
+}
 
 int device_sm_count();      // SMs of the current device (cached per device)
 bool device_is_sm103();     // current device is compute capability 10.3

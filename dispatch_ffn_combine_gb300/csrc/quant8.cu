@@ -251,6 +251,7 @@ extern "C" mk_status mk_moe_quant8_weights(const void* w, int E, int n, int d, u
                                            void* stream) {
     const mk_status st = check_sizes(0, d, E, 1, n);
     if (st != MK_OK) return st;
+    if (n >= 1 << 30 || d >= 1 << 30) return MK_ERR_UNSUPPORTED;  // rows and columns are counted in 32 bits, a block's past the end included
     if (!w || !codes || !scales || !aligned16(w) || !aligned16(codes) || !aligned16(scales)) return MK_ERR_INVALID_ARG;
     const int k_blocks = (d + kScaleBlock - 1) / kScaleBlock, n_blocks = (n + kScaleBlock - 1) / kScaleBlock;
     if (static_cast<int64_t>(k_blocks) * n_blocks >= (int64_t(1) << 31)) return MK_ERR_UNSUPPORTED;

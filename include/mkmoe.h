@@ -602,7 +602,7 @@ MK_API mk_status mk_moe_quant8_rows(const void* x, int64_t ld, int64_t S, int c,
 
 /* Weights in that form, a scale for each block of 128 x 128:
  *   w bf16 [E, n, d]; codes uint8 [E, n, d] (out); scales fp32 [E, ceil(n / 128), pitch(d)] (out)
- * Limits as for mk_moe_grouped_gemm's weights. */
+ * Limits as for mk_moe_grouped_gemm's weights, and n, d < 2^30. */
 MK_API mk_status mk_moe_quant8_weights(const void* w, int E, int n, int d, uint8_t* codes, float* scales, void* stream);
 
 /* SwiGLU between two 8-bit products: silu(gate) * up in that form, worked out in fp32 as
@@ -640,7 +640,7 @@ MK_API mk_status mk_moe_dispatch8(const uint8_t* codes, const float* scales, con
  * The products of the codes are exact and each block's sum of 128 of them is
  * the tensor core's; blocks are joined in fp32.  Scales may have any value of
  * which a row's times a weight block's is a normal fp32 number (or zero).
- * Limits and bad offsets as in mk_moe_grouped_gemm. */
+ * Limits and bad offsets as in mk_moe_grouped_gemm, and d < 2^28, n < 2^30. */
 MK_API mk_status mk_moe_grouped_gemm8(const uint8_t* codes, const float* scales, const int32_t* expert_offsets,
                                const uint8_t* w_codes, const float* w_scales, const float* row_weight, int64_t S,
                                int d, int E, int n, void* out, int out_type, void* ws, size_t ws_bytes, void* stream);
