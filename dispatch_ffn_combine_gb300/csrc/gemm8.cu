@@ -764,8 +764,11 @@ extern "C" mk_status mk_moe_grouped_gemm8(const uint8_t* codes, const float* sca
                                           const uint8_t* w_codes, const float* w_scales, const float* row_weight,
                                           int64_t S, int d, int E, int n, void* out, int out_type, void* ws,
                                           size_t ws_bytes, void* stream) {
-    const mk_status st = check_sizes(S, d, E, 1, n);
+    const mk_status st = check_sizes(0, d, E, 1, n);
     if (st != MK_OK) return st;
+    if (S < 0) return MK_ERR_INVALID_ARG;
+    // Rows and columns are 32-bit coordinates each, offsets in 64 bits: eight rows for each of four million tokens, of any length.
+    if (S >= 1 << 25 || S * std::max(d, n) >= (int64_t(1) << 40)) return MK_ERR_UNSUPPORTED;
     // Columns are counted in 32 bits, a tile's past the end included; and a tile of 2^28 columns takes 1.2 s, a longer
     // one more than the bounded waits for its end allow.
     if (d >= 1 << 28 || n >= 1 << 30) return MK_ERR_UNSUPPORTED;

@@ -640,7 +640,8 @@ MK_API mk_status mk_moe_dispatch8(const uint8_t* codes, const float* scales, con
  * The products of the codes are exact and each block's sum of 128 of them is
  * the tensor core's; blocks are joined in fp32.  Scales may have any value of
  * which a row's times a weight block's is a normal fp32 number (or zero).
- * Limits and bad offsets as in mk_moe_grouped_gemm, and d < 2^28, n < 2^30. */
+ * Bad offsets as in mk_moe_grouped_gemm.  Limits: d and n multiples of 64, d < 2^28,
+ * n < 2^30, E * max(d, n) < 2^31, S < 2^25, S * max(d, n) < 2^40. */
 MK_API mk_status mk_moe_grouped_gemm8(const uint8_t* codes, const float* scales, const int32_t* expert_offsets,
                                const uint8_t* w_codes, const float* w_scales, const float* row_weight, int64_t S,
                                int d, int E, int n, void* out, int out_type, void* ws, size_t ws_bytes, void* stream);

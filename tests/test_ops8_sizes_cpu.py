@@ -31,6 +31,13 @@ def test_product_refuses_what_its_counters_do_not_hold(lib, S, d, E, n):
     assert _gemm8(lib, S, d, E, n) == mk.MK_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("S,d,E,n", [(8 * 131072, 7168, 256, 4096), (8 * 131072, 2048, 256, 7168), (320000, 7168, 256, 4096),
+                                     ((1 << 25) - 1, 64, 8, 64), ((1 << 25) - 1, 16384, 8, 16384), (1, (1 << 28) - 64, 1, 64)])
+def test_product_takes_the_rows_of_every_token_the_layer_takes(lib, S, d, E, n):
+    """128K tokens of the large layer among them: eight rows each, more than 2^31 values."""
+    assert _gemm8(lib, S, d, E, n) == mk.MK_ERR_WORKSPACE
+
+
 @pytest.mark.parametrize("n,d", [(1 << 30, 64), (64, 1 << 30), (64, (1 << 31) - 64)])
 def test_weights_quantiser_refuses_as_the_rows_do(lib, n, d):
     assert lib.mk_moe_quant8_weights(None, 1, n, d, A, A, None) == mk.MK_ERR_UNSUPPORTED
