@@ -196,24 +196,33 @@ __device__ __forceinline__ bool take_slot_one(Ctl8* ctl, SlotCursor& cur, int4& 
     return true;
 }
 
-// A whole warp's bounded wait, with one uniform branch where the phase is complete already.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile uint32_t* abort_word,
-                                          uint64_t timeout_ns) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// A whole warp's bounded wait, with one uniform branch where the phase is complete already; _cluster: for barriers that
+// the peer CTA's threads, copies or commits complete.
+template <typename Try>
+__device__ __forceinline__ bool warp_wait_with(Try try_wait, const volatile uint32_t* abort_word, uint64_t timeout_ns) {
+    if (__all_sync(0xffffffffu, try_wait())) return true;
     const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
     for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, try_wait())) return true;
         if ((it & 31u) == 0u && __any_sync(0xffffffffu, *abort_word != 0u || globaltimer_ns() - t0 > timeout_ns)) return false;
     }
 }
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile uint32_t* abort_word,
+                                          uint64_t timeout_ns) {
+    return warp_wait_with([&] { return mbar_try_wait(bar, parity); }, abort_word, timeout_ns);
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, const volatile uint32_t* abort_word,
+                                                  uint64_t timeout_ns) {
+    return warp_wait_with([&] { return mbar_try_wait_cluster(bar, parity); }, abort_word, timeout_ns);
+}
 
 // Whether a phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n_row1 = w_row + 128 + static_cast<int>(rank) * (size1 >> 1);
                     const uint32_t stage_tx = static_cast<uint32_t>(box0 + box1 + 2 * 64 * parts) * kBlockK;
                     for (int kb = 0; kb < p.k_blocks; ++kb) {
-                        if (!(ok = mbar_wait_bounded(smem_u32(&ctl->empty[st.stage]), st.phase ^ 1u, abort_word, p.timeout_ns)))
+                        if (!(ok = mbar_wait_bounded_cluster(smem_u32(&ctl->empty[st.stage]), st.phase ^ 1u, abort_word, p.timeout_ns)))
                             break;
                         const uint32_t sa = smem_u32(smem + st.stage * kStageBytes);
                         const uint32_t fb = full0 + st.stage * 8u;
@@ -418,12 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t idesc0 = idesc_e4m3_f32(PAIR_M, static_cast<uint32_t>(min(128, cols)));
                     const uint32_t idesc1 = idesc_e4m3_f32(PAIR_M, static_cast<uint32_t>(parts == 2 ? cols - 128 : 128));
                     for (int kb = 0; kb < p.k_blocks && ok; ++kb) {
-                        if (!(ok = mbar_wait_bounded(smem_u32(&ctl->full[st.stage]), st.phase, abort_word, p.timeout_ns))) break;
+                        if (!(ok = mbar_wait_bounded_cluster(smem_u32(&ctl->full[st.stage]), st.phase, abort_word, p.timeout_ns))) break;
                         const uint64_t ad = desc0 + st.stage * (kStageBytes >> 4);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (h >= parts) continue;
-                            if (!(ok = ok && mbar_wait_bounded(smem_u32(&ctl->tmem_empty[acc[h].acc]), acc[h].phase ^ 1u,
+                            if (!(ok = ok && mbar_wait_bounded_cluster(smem_u32(&ctl->tmem_empty[acc[h].acc]), acc[h].phase ^ 1u,
                                                                abort_word, p.timeout_ns)))
                                 break;
                             tc_fence_after();
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ready = false;
         auto acc_wait = [&]() {
             const bool r = ready ||
-                           warp_wait(smem_u32(&ctl->tmem_full[acc.acc]), acc.phase, abort_word, p.timeout_ns);
+                           warp_wait_cluster(smem_u32(&ctl->tmem_full[acc.acc]), acc.phase, abort_word, p.timeout_ns);
             tc_fence_after();
             return r;
         };
@@ -619,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                         if (c + 32 == kBlockN) {
                             acc_release();
-                            ready = __all_sync(0xffffffffu, mbar_test(smem_u32(&ctl->tmem_full[acc.acc]), acc.phase));
+                            ready = __all_sync(0xffffffffu, mbar_test_cluster(smem_u32(&ctl->tmem_full[acc.acc]), acc.phase));
                         }
 #pragma unroll
                         for (int q = 0; q < 32; q += 2) fma2(sum[c + q], sum[c + q + 1], v[q], v[q + 1], scale2);
