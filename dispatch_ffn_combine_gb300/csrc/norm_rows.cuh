@@ -273,10 +273,10 @@ struct RingPart {
 
 // The blocks' partial rows [blocks][n] added, 32 columns per block: 8 slices of
 // every eighth partial row, then the slices in order.  Columns below `split` go
-// to `first`, the others to `second`.
+// to `first`, the others to `second`; with `add` onto what is there.
 static __global__ void __launch_bounds__(256) sum_partial_rows_kernel(const float* __restrict__ part, int blocks, int n,
                                                                       int split, float* __restrict__ first,
-                                                                      float* __restrict__ second) {
+                                                                      float* __restrict__ second, bool add) {
     __shared__ float s[8][32];
     pdl_wait();  // the partial rows come from the kernel before
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
@@ -290,7 +290,8 @@ static __global__ void __launch_bounds__(256) sum_partial_rows_kernel(const floa
     if (slice == 0 && c < n) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) v += s[i][lane];
-        (c < split ? first + c : second + (c - split))[0] = v;
+        float* to = c < split ? first + c : second + (c - split);
+        *to = add ? *to + v : v;
     }
 }
 
@@ -298,9 +299,9 @@ static __global__ void __launch_bounds__(256) sum_partial_rows_kernel(const floa
 
 // Behind the kernel that writes the partial rows, as its programmatic dependent.
 static inline cudaError_t sum_partial_rows(const float* part, int blocks, int n, int split, float* first, float* second,
-                                           cudaStream_t s) {
+                                           cudaStream_t s, bool add = false) {
     const LaunchCfg lc(dim3(static_cast<unsigned>((static_cast<int64_t>(n) + 31) / 32)), dim3(256), 0, s, true);
-    const cudaError_t err = cudaLaunchKernelEx(&lc.cfg, sum_partial_rows_kernel, part, blocks, n, split, first, second);
+    const cudaError_t err = cudaLaunchKernelEx(&lc.cfg, sum_partial_rows_kernel, part, blocks, n, split, first, second, add);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -367,6 +368,13 @@ inline int grid_blocks(const RowShape& s, int64_t rows, int d, int most) {
     const int apart = 8 / std::gcd(d, 8), unit = apart / std::gcd(s.rows, apart);
     return std::max(unit, most / unit * unit);
 }
+
+// Rows that a row group of a backward pass adds up in one fp32 sum per column.  A chain of n additions is off by up to n
+// 2^-24 of its terms' magnitudes, so more rows than that per group (a million for long rows, ten for short ones) go through the
+// kernel in pieces, whose sums are added: 2^-12 for a piece and 2^-24 for each.  The rows of a piece are a multiple of 8, so that it
+// starts on a 16-byte word as the tensor does.
+constexpr int kMaxChain = 4096;
+inline int64_t piece_rows(const RowShape& s, int blocks) { return static_cast<int64_t>(kMaxChain) * s.rows * blocks; }
 
 // Leave for `fn`'s launches to use up to kSmSmem of shared memory, once per device.
 // The attribute is the function's, not the launch's: set to each call's own need, a

@@ -284,8 +284,7 @@ struct RmsArgs {
     const float* rstd;
     const void *dy, *dres;
     void* dx;
-    float* part;
-    int blocks;  // out: partial rows written
+    float *part, *dgamma;
 };
 
 // A ring of three stages, with fewer rows per block where they do not fit; two for
@@ -333,20 +332,28 @@ cudaError_t run_fwd(const RmsArgs& a) {
 }
 
 template <typename T, int NV, bool kAligned, int STAGES>
-cudaError_t launch_bwd(RmsArgs& a, const RowShape& r, const Ring& q) {
+cudaError_t launch_bwd(const RmsArgs& a, const RowShape& r, const Ring& q) {
     const size_t smem = std::max(q.bytes, sizeof(float) * static_cast<size_t>(a.d) * r.rows);
-    a.blocks = grid_blocks(r, a.rows, a.d, std::min(q.blocks * device_sm_count(), kMaxBwdBlocks));
+    const int most = std::min(q.blocks * device_sm_count(), kMaxBwdBlocks);
     constexpr auto fn = rmsnorm_bwd_kernel<T, NV, kAligned, STAGES>;
-    const cudaError_t err = allow_smem<fn>();
-    if (err != cudaSuccess) return err;
-    fn<<<a.blocks, r.threads(), smem, a.s>>>(static_cast<const bf16*>(a.dy), static_cast<const T*>(a.x), a.gamma, a.rstd,
-                                             static_cast<const T*>(a.dres), a.rows, a.d, r.warps, static_cast<T*>(a.dx),
-                                             a.part);
-    return cudaGetLastError();
+    cudaError_t err = allow_smem<fn>();
+    const int64_t piece = piece_rows(r, grid_blocks(r, a.rows, a.d, most));
+    for (int64_t row = 0; row < a.rows && err == cudaSuccess; row += piece) {
+        const int rows = static_cast<int>(std::min<int64_t>(piece, a.rows - row));
+        const int64_t at = row * a.d;
+        const int blocks = grid_blocks(r, rows, a.d, most);
+        const T* dres = static_cast<const T*>(a.dres);
+        fn<<<blocks, r.threads(), smem, a.s>>>(static_cast<const bf16*>(a.dy) + at, static_cast<const T*>(a.x) + at, a.gamma,
+                                               a.rstd + row, dres != nullptr ? dres + at : nullptr, rows, a.d, r.warps,
+                                               static_cast<T*>(a.dx) + at, a.part);
+        err = cudaGetLastError();
+        if (err == cudaSuccess) err = sum_partial_rows(a.part, blocks, a.d, a.d, a.dgamma, nullptr, a.s, row > 0);
+    }
+    return err;
 }
 
 template <typename T, bool kAligned>
-cudaError_t run_bwd(RmsArgs& a) {
+cudaError_t run_bwd(const RmsArgs& a) {
     RowShape r = row_shape(a.rows, a.d, false);
     const int xs = a.dres != nullptr ? 2 : 1;
     const Ring q = ring_shape(r, r.nv * (RingPart<T, 1>::kWords * xs + RingPart<bf16, 1>::kWords));
@@ -361,7 +368,7 @@ cudaError_t run_bwd(RmsArgs& a) {
 }
 
 template <typename T>
-cudaError_t run_bwd(RmsArgs& a) {
+cudaError_t run_bwd(const RmsArgs& a) {
     return a.d % 8 == 0 ? run_bwd<T, true>(a) : run_bwd<T, false>(a);
 }
 
@@ -423,6 +430,6 @@ extern "C" mk_status mk_moe_rmsnorm_bwd(const void* dy, const void* h, int x_typ
     a.x = h, a.gamma = gamma, a.rows = static_cast<int>(T), a.d = d, a.s = s;
     a.rstd = rstd, a.dy = dy, a.dres = dres, a.dx = dx;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    if ((x_type == MK_TYPE_FP32 ? run_bwd<float>(a) : run_bwd<bf16>(a)) != cudaSuccess) return MK_ERR_CUDA;
-    return sum_partial_rows(a.part, a.blocks, d, d, dgamma, nullptr, s) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    a.dgamma = dgamma;
+    return (x_type == MK_TYPE_FP32 ? run_bwd<float>(a) : run_bwd<bf16>(a)) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

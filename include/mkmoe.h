@@ -531,7 +531,8 @@ MK_API size_t mk_moe_rmsnorm_bwd_workspace_size(int64_t T, int d);
 
 /* Its backward pass, with t = dy gamma:
  *   dx = rstd t - h rstd^3 sum(t h) / d (+ dres)   in h's type: the gradient of x, and of add
- *   dgamma = sum over rows of dy h rstd   (one fixed order)
+ *   dgamma = sum over rows of dy h rstd   (one fixed order; no fp32 sum is a chain of
+ *        more than 4096 rows)
  *   dy bf16 [T, d]; h [T, d] what the norm took (x without add); dres [T, d] in h's
  *   type or NULL: a gradient that reaches h past the norm; dx [T, d] (out);
  *   dgamma fp32 [d] (out; zeros when T == 0) */
