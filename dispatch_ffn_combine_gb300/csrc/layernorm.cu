@@ -279,8 +279,7 @@ struct NormArgs {
     // backward
     const void *dy, *dres;
     void* dx;
-    float* part;
-    int blocks;  // out: partial rows written
+    float *part, *dgamma, *dbeta;
 };
 
 template <typename T, int NV, bool kAligned>
@@ -304,20 +303,28 @@ cudaError_t run_fwd(const NormArgs& a) {
 }
 
 template <typename T, int NV, bool kAligned, int STAGES>
-cudaError_t launch_bwd(NormArgs& a, const RowShape& r, const Ring& q) {
+cudaError_t launch_bwd(const NormArgs& a, const RowShape& r, const Ring& q) {
     const size_t smem = std::max(q.bytes, 2 * sizeof(float) * static_cast<size_t>(a.d) * r.rows);
-    a.blocks = grid_blocks(r, a.rows, a.d, std::min(q.blocks * device_sm_count(), kMaxBwdBlocks));
+    const int most = std::min(q.blocks * device_sm_count(), kMaxBwdBlocks);
     constexpr auto fn = layernorm_bwd_kernel<T, NV, kAligned, STAGES>;
-    const cudaError_t err = allow_smem<fn>();
-    if (err != cudaSuccess) return err;
-    fn<<<a.blocks, r.threads(), smem, a.s>>>(static_cast<const bf16*>(a.dy), static_cast<const T*>(a.x), a.gamma,
-                                             a.mean, a.rstd, static_cast<const T*>(a.dres), a.rows, a.d, r.warps,
-                                             static_cast<T*>(a.dx), a.part);
-    return cudaGetLastError();
+    cudaError_t err = allow_smem<fn>();
+    const int64_t piece = piece_rows(r, grid_blocks(r, a.rows, a.d, most));
+    for (int64_t row = 0; row < a.rows && err == cudaSuccess; row += piece) {
+        const int rows = static_cast<int>(std::min<int64_t>(piece, a.rows - row));
+        const int64_t at = row * a.d;
+        const int blocks = grid_blocks(r, rows, a.d, most);
+        const T* dres = static_cast<const T*>(a.dres);
+        fn<<<blocks, r.threads(), smem, a.s>>>(static_cast<const bf16*>(a.dy) + at, static_cast<const T*>(a.x) + at, a.gamma,
+                                               a.mean + row, a.rstd + row, dres != nullptr ? dres + at : nullptr, rows, a.d,
+                                               r.warps, static_cast<T*>(a.dx) + at, a.part);
+        err = cudaGetLastError();
+        if (err == cudaSuccess) err = sum_partial_rows(a.part, blocks, 2 * a.d, a.d, a.dgamma, a.dbeta, a.s, row > 0);
+    }
+    return err;
 }
 
 template <typename T, bool kAligned>
-cudaError_t run_bwd(NormArgs& a) {
+cudaError_t run_bwd(const NormArgs& a) {
     RowShape r = row_shape(a.rows, a.d, false);
     const int xs = a.dres != nullptr ? 2 : 1;
     const Ring q = ring_shape(r, r.nv * (RingPart<T, 1>::kWords * xs + RingPart<bf16, 1>::kWords));
@@ -332,7 +339,7 @@ cudaError_t run_bwd(NormArgs& a) {
 }
 
 // The kernels for x's type and for rows that start a 16-byte word or not.
-cudaError_t run(NormArgs& a, int x_type, bool forward) {
+cudaError_t run(const NormArgs& a, int x_type, bool forward) {
     const bool aligned = a.d % 8 == 0;
     if (x_type == MK_TYPE_FP32)
         return forward ? (aligned ? run_fwd<float, true>(a) : run_fwd<float, false>(a))
@@ -400,6 +407,6 @@ extern "C" mk_status mk_moe_layernorm_bwd(const void* dy, const void* x, int x_t
     a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
     a.dy = dy, a.dres = dres, a.dx = dx;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    if (run(a, x_type, false) != cudaSuccess) return MK_ERR_CUDA;
-    return sum_partial_rows(a.part, a.blocks, 2 * d, d, dgamma, dbeta, s) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    a.dgamma = dgamma, a.dbeta = dbeta;
+    return run(a, x_type, false) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

@@ -505,7 +505,8 @@ MK_API size_t mk_moe_layernorm_bwd_workspace_size(int64_t T, int d);
 
 /* Its backward pass, with xh = (x - mean) rstd and t = dy gamma:
  *   dx = rstd (t - sum t / d - xh sum(t xh) / d) (+ dres)   in x's type
- *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy   (one fixed order)
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy   (one fixed order; no
+ *        fp32 sum is a chain of more than 4096 rows)
  *   dy bf16 [T, d]; dres [T, d] in x's type or NULL: a gradient that reaches x
  *   past the norm (the residual stream); dx [T, d] (out); dgamma, dbeta fp32 [d] (out; zeros when T == 0) */
 MK_API mk_status mk_moe_layernorm_bwd(const void* dy, const void* x, int x_type, const float* gamma,

@@ -31,6 +31,20 @@ def test_norm_weight_gradient_of_many_equal_rows(T, d):
         float((dgamma.to(F64) / want - 1).abs().max())
 
 
+@pytest.mark.parametrize("T,d", [(3 << 26, 3), (1 << 22, 1001)])
+def test_layer_norm_weight_gradients_of_many_equal_rows(T, d):
+    """As above: dgamma's term is (x - mean) rstd dy, dbeta's dy."""
+    _room(3 * 2 * T * d / 1e9 + 8)
+    x = torch.ones((T, d), dtype=BF, device=DEV)
+    dy = torch.full((T, d), 1 / 3, dtype=BF, device=DEV)
+    gamma = torch.ones(d, device=DEV)
+    mean, rstd = torch.full((T,), 0.25, device=DEV), torch.full((T,), 0.9, device=DEV)
+    _, dgamma, dbeta = mk.mk_moe_layernorm_bwd(dy, x, gamma, mean, rstd)
+    tol = 2.0 ** -22 + (4096 + 16 + 304 + 64) * 2.0 ** -24
+    for got, term in ((dgamma, 0.75 * float(rstd[0]) * float(dy[0, 0])), (dbeta, float(dy[0, 0]))):
+        assert bool(((got.to(F64) / (T * term) - 1).abs() <= tol).all()), float((got.to(F64) / (T * term) - 1).abs().max())
+
+
 def test_norm_weight_gradient_in_pieces_is_the_rows_own():
     """More rows than one piece, values of both signs and a ragged end: every row counts once, dx is each row's own."""
     _room(12)
