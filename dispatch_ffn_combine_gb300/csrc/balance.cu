@@ -41,12 +41,16 @@ constexpr int kLanes = 8;        // of a token
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kPass = kThreads / kLanes;  // tokens a block takes at a time
-constexpr int kMaxBlocks = 608;  // partial rows, and blocks of the backward kernel: four per SM
+constexpr int kManyBlocks = 608;  // partial rows, and blocks of the backward kernel: four per SM
+// Tokens whose p a lane adds up in one fp32 sum: a chain of n additions is off by up to n 2^-24, so beyond 20 million
+// tokens there are more blocks rather than longer chains (65536 of them at most, whose partial rows the sums' kernel
+// adds in slices of 2048 at most).
+constexpr int kMaxChain = 2048;
 constexpr int kMaxSlices = 32;   // of a sequence's partial rows, a warp each
 constexpr int kMaxSeqs = 65535;
 
 int tokens_per_block(int64_t T) {
-    return static_cast<int>(std::max<int64_t>(kPass, (T + kMaxBlocks - 1) / kMaxBlocks));
+    return static_cast<int>(std::min<int64_t>(kPass * kMaxChain, std::max<int64_t>(kPass, (T + kManyBlocks - 1) / kManyBlocks)));
 }
 
 struct Seqs {
@@ -536,7 +540,8 @@ extern "C" mk_status mk_moe_balance_loss(const float* logits, const int32_t* top
     if (err != cudaSuccess) return MK_ERR_CUDA;
     // With few long sequences a block's own walk is the time (32768 tokens of 256 experts in one: 29 us with 8 slices,
     // 19 with 32), with many the blocks (512 sequences of 256 tokens, 64 experts: 21 and 30).
-    const unsigned slices = blocks > 64 * B ? kMaxSlices : 8;
+    // So many blocks may be one sequence's that eight slices would be longer chains than a lane's.
+    const unsigned slices = blocks > std::min(64 * B, 8 * kMaxChain) ? kMaxSlices : 8;
     LaunchCfg lc(dim3(static_cast<unsigned>((E + 31) / 32), static_cast<unsigned>(B)), dim3(32u * slices), 0, s, true);
     if (cudaLaunchKernelEx(&lc.cfg, balance_sum_kernel, part, seqs, E, k, per_block, loss, counts, probs, terms, status) !=
         cudaSuccess)

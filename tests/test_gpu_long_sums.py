@@ -1,5 +1,5 @@
-"""Sums over very many rows: the longest chain of fp32 additions does not grow with them.  Terms that are all
-alike round the same way at every step, the worst a chain can do.  2 to 15 GB on the device; skipped where that is not free."""
+"""Sums over very many tokens or rows: the longest chain of fp32 additions does not grow with them.  Terms that are all
+alike round the same way at every step, the worst a chain can do.  2 to 45 GB on the device; skipped where that is not free."""
 import pytest
 import torch
 
@@ -66,3 +66,20 @@ def test_norm_weight_gradient_in_pieces_is_the_rows_own():
     assert bool(((dgamma.to(F64) - want).abs() <= mag * (2.0 ** -22 + (4096 + 16 + 304 + 64) * 2.0 ** -24)).all())
     again = mk.mk_moe_rmsnorm_bwd(dy, h, gamma, rstd, dres=dy)[1]
     assert torch.equal(again, dgamma)
+
+
+@pytest.mark.parametrize("T,E", [(3 << 28, 3), (3 << 28, 9), (1 << 24, 100)])
+def test_router_losses_of_many_equal_tokens(T, E):
+    """p = 1 / E and lse = log E for every token, each within 2^-21 of itself.  A lane adds 2048 tokens at most, then
+    come 16 groups, 2048 partial rows a slice and 32 slices, and for the losses a tree: 2^-24 of the sum each."""
+    _room(4 * T * E / 1e9 + 12)
+    logits = torch.zeros((T, E), device=DEV)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    loss, counts, probs = mk.mk_moe_balance_loss(logits, ids)
+    assert counts[0].tolist() == [T] + [0] * (E - 1)
+    tol = 2.0 ** -20 + (2048 + 16 + 2048 + 32 + 64) * 2.0 ** -24
+    assert bool(((probs.to(F64) * E - 1).abs() <= tol).all()), float((probs.to(F64) * E - 1).abs().max())
+    # sum_e E counts_e / T probs_e = E probs_0
+    assert abs(float(loss[0]) - 1) <= tol + 2.0 ** -21
+    lse2 = float(torch.log(torch.tensor(float(E), dtype=F64)) ** 2)
+    assert abs(float(loss[1]) / lse2 - 1) <= tol + 2.0 ** -20
