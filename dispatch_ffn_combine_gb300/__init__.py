@@ -743,6 +743,15 @@ def mk_moe_swiglu_ckpt8_bwd(dh, codes, scales, row_weight=None, dgate=None, dup=
     return dgate, dup, hw, drow_weight
 
 
+def _written(out, wanted):
+    """`out` as a dict, if it holds nothing (but None) that the call does not write."""
+    out = out or {}
+    for name, t in out.items():
+        if t is not None and name not in wanted:
+            raise ValueError(f"out[{name!r}] is not an output of this call")
+    return out
+
+
 def _norm_rows(x):
     T, d = _dims(x, "x", 2)
     if x.dtype not in _TYPES:
@@ -788,12 +797,11 @@ def mk_moe_rmsnorm(x, gamma, eps=1e-5, add=None, bits8=False, bf16=True, out=Non
 
     x [T, d] bf16 or fp32, add [T, d] bf16 or None, gamma [d] fp32.  Returns dict(h [T, d] in x's type (x
     itself without add), y [T, d] bf16 or None without bf16, rstd [T] fp32, and with bits8 the output as codes
-    [T, d] uint8 and scales [T, scale_pitch(d)] fp32, else None).  `out` may hold any of these to be written;
-    its h may be x."""
+    [T, d] uint8 and scales [T, scale_pitch(d)] fp32, else None).  `out` may hold any of these that the call writes
+    (h only with add, y, codes and scales only where they are wanted); its h may be x, or add where both are bf16."""
     T, d = _norm_rows(x)
     if not bf16 and not bits8:
         raise ValueError("mk_moe_rmsnorm needs bf16 or bits8")
-    out = out or {}
     wanted = {"rstd": (_F32, (T,))}
     if add is not None:
         wanted["h"] = (x.dtype, (T, d))
@@ -801,6 +809,9 @@ def mk_moe_rmsnorm(x, gamma, eps=1e-5, add=None, bits8=False, bf16=True, out=Non
         wanted["y"] = (_BF, (T, d))
     if bits8:
         wanted["codes"], wanted["scales"] = (_U8, (T, d)), (_F32, (T, scale_pitch(d)))
+    if add is None and out and out.get("h") is x:  # as a call without add returns it
+        out = {**out, "h": None}
+    out = _written(out, wanted)
     _inputs(x, (x, x.dtype, (T, d), "x"), (gamma, _F32, (d,), "gamma"), (add, _BF, (T, d), "add"),
             *((out.get(name), dtype, shape, name) for name, (dtype, shape) in wanted.items()))
     r = {"h": x, "y": None, "codes": None, "scales": None,
@@ -952,7 +963,7 @@ def mk_moe_dispatch8(codes, scales, topk_ids, topk_w, E, out=None, ws=None, stre
     pitch = scale_pitch(d)
     wanted = {"expert_offsets": (_I32, (E + 1,)), "row_token": (_I32, (T * k,)), "row_weight": (_F32, (T * k,)),
               "slot_row": (_I32, (T, k)), "codes": (_U8, (T * k, d)), "scales": (_F32, (T * k, pitch))}
-    out = out or {}
+    out = _written(out, wanted)
     _inputs(codes, (codes, _U8, (T, d), "codes"), (scales, _F32, (T, pitch), "scales"),
             (topk_ids, _I32, (T, k), "topk_ids"), (topk_w, _F32, (T, k), "topk_w"),
             *((out.get(name), dtype, shape, f"out[{name!r}]") for name, (dtype, shape) in wanted.items()))
