@@ -166,7 +166,7 @@ cudaError_t launch_grouped_gemm(const bf16* x_perm, const int32_t* offsets, cons
 
 // Workspace of the 8-bit dispatch: the control block and the tables of the counting steps.
 struct Dispatch8Layout {
-    size_t chunk_counts, chunk_base, rank, counts, mtile_start, total;
+    size_t chunk_counts, chunk_base, rank, counts, total;
 };
 Dispatch8Layout dispatch8_layout(int64_t T, int E, int k) {
     Dispatch8Layout L{};
@@ -181,7 +181,6 @@ Dispatch8Layout dispatch8_layout(int64_t T, int E, int k) {
     L.chunk_base = take(chunk_words);
     L.rank = take(static_cast<size_t>(T) * k);
     L.counts = take(E);
-    L.mtile_start = take(E + 1);
     L.total = at;
     return L;
 }
@@ -300,10 +299,9 @@ mk_status mk_moe_dispatch8(const uint8_t* codes, const float* scales, const int3
     uint32_t* status = at<uint32_t>(ws, 0);
     int32_t* chunk_base = nullptr;
     int32_t* rank = at<int32_t>(ws, L.rank);
-    int32_t* mtile_start = at<int32_t>(ws, L.mtile_start);
     // Each kernel but the first is a programmatic dependent of the one before.
     if (T > 0 && T <= kSmallTokens) {
-        MK_TRY(launch_small_tables(topk_ids, T, E, k, rank, expert_offsets, mtile_start, status, s));
+        MK_TRY(launch_small_tables(topk_ids, T, E, k, rank, expert_offsets, status, s));
     } else {
         MK_TRY(launch_clear_control(status, s));  // status, site, scan ticket
         if (T == 0) {
@@ -314,7 +312,7 @@ mk_status mk_moe_dispatch8(const uint8_t* codes, const float* scales, const int3
         chunk_base = at<int32_t>(ws, L.chunk_base);
         MK_TRY(launch_count(topk_ids, T, E, k, chunk_counts, rank, status, s, true));
         MK_TRY(launch_scan(chunk_counts, num_chunks(T), E, chunk_base, at<int32_t>(ws, L.counts), expert_offsets,
-                           mtile_start, status + 3, s, true));
+                           nullptr, status + 3, s, true));
     }
     MK_TRY(launch_scatter8(codes, scales, topk_ids, topk_w, T, d, E, k, expert_offsets, chunk_base, rank, codes_perm,
                            scales_perm, row_token, row_weight, slot_row, s));

@@ -72,7 +72,7 @@ __device__ __forceinline__ int warp_inclusive_scan(int v, int lane) {
 }
 
 // Exclusive scans over experts, by one warp (E <= 256: 8 experts per lane).
-// Writes offsets[0..E] and mtile_start[0..E] from per-expert counts in smem.
+// Writes offsets[0..E] and (unless null) mtile_start[0..E] from per-expert counts in smem.
 __device__ void expert_scan_warp(const int32_t* s_counts, int E, int lane, int32_t* offsets, int32_t* mtile_start) {
     int cnt[8];
     int til[8];
@@ -93,14 +93,14 @@ __device__ void expert_scan_warp(const int32_t* s_counts, int E, int lane, int32
         const int e = lane * 8 + i;
         if (e < E) {
             offsets[e] = run_c;
-            mtile_start[e] = run_t;
+            if (mtile_start != nullptr) mtile_start[e] = run_t;
         }
         run_c += cnt[i];
         run_t += til[i];
     }
     if (lane == 31) {
         offsets[E] = inc_c;
-        mtile_start[E] = inc_t;
+        if (mtile_start != nullptr) mtile_start[E] = inc_t;
     }
 }
 
@@ -111,7 +111,7 @@ __device__ void expert_scan_warp(const int32_t* s_counts, int E, int lane, int32
 constexpr int kSmallWords = kSmallTokens / 32;
 __global__ void __launch_bounds__(1024) small_tables_kernel(const int32_t* __restrict__ ids, int T, int E, int k,
                                                             int32_t* __restrict__ rank, int32_t* __restrict__ offsets,
-                                                            int32_t* __restrict__ mtile_start, uint32_t* status) {
+                                                            uint32_t* status) {
     __shared__ uint32_t mask[kMaxExperts][kSmallWords + 1];  // one more: experts' words on different banks
     __shared__ int32_t s_counts[kMaxExperts];
     pdl_launch_dependents();
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(1024) small_tables_kernel(const int32_t* __res
         rank[q] = r;
     }
     __syncthreads();
-    if (threadIdx.x < 32) expert_scan_warp(s_counts, E, threadIdx.x, offsets, mtile_start);
+    if (threadIdx.x < 32) expert_scan_warp(s_counts, E, threadIdx.x, offsets, nullptr);
 }
 
 // Scans after counting.  Block g takes experts [32 g, 32 g + 32), one per lane
@@ -383,8 +383,8 @@ cudaError_t launch_scan(const int32_t* chunk_counts, int64_t nchunks, int E, int
 }
 
 cudaError_t launch_small_tables(const int32_t* ids, int64_t T, int E, int k, int32_t* rank, int32_t* offsets,
-                                int32_t* mtile_start, uint32_t* status, cudaStream_t s) {
-    small_tables_kernel<<<1, 1024, 0, s>>>(ids, static_cast<int>(T), E, k, rank, offsets, mtile_start, status);
+                                uint32_t* status, cudaStream_t s) {
+    small_tables_kernel<<<1, 1024, 0, s>>>(ids, static_cast<int>(T), E, k, rank, offsets, status);
     return cudaGetLastError();
 }
 

@@ -153,6 +153,7 @@ cudaError_t launch_topk(const float* logits, int64_t T, int E, int k, int32_t* i
 cudaError_t launch_count(const int32_t* ids, int64_t T, int E, int k, int32_t* chunk_counts, int32_t* rank,
                          uint32_t* status, cudaStream_t s, bool pdl = false);
 // `done`: a zeroed word (left zero again) that picks the last block for the expert scan.
+// mtile_start null: no tile table.
 cudaError_t launch_scan(const int32_t* chunk_counts, int64_t nchunks, int E, int32_t* chunk_base, int32_t* counts,
                         int32_t* offsets, int32_t* mtile_start, uint32_t* done, cudaStream_t s, bool pdl = false);
 cudaError_t launch_scatter(const bf16* x, const int32_t* ids, const float* w, int64_t T, int d, int E, int k,
@@ -160,9 +161,9 @@ cudaError_t launch_scatter(const bf16* x, const int32_t* ids, const float* w, in
                            int32_t* row_token, float* row_weight, int32_t* slot_row, cudaStream_t s,
                            const TileSems* sem = nullptr, const int32_t* mtile_start = nullptr,
                            bool copy_rows = true);
-// launch_clear_control, launch_count and launch_scan in one launch, for T <= kSmallTokens; ranks need no chunk bases.
+// launch_clear_control, launch_count and launch_scan (without the tile table) in one launch, for T <= kSmallTokens; ranks need no chunk bases.
 cudaError_t launch_small_tables(const int32_t* ids, int64_t T, int E, int k, int32_t* rank, int32_t* offsets,
-                                int32_t* mtile_start, uint32_t* status, cudaStream_t s);
+                                uint32_t* status, cudaStream_t s);
 // chunk_base null: one chunk.
 cudaError_t launch_scatter8(const uint8_t* codes, const float* scales, const int32_t* ids, const float* w, int64_t T,
                             int d, int E, int k, const int32_t* offsets, const int32_t* chunk_base, const int32_t* rank,
