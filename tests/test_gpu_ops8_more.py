@@ -60,3 +60,20 @@ def test_sum_over_the_added_tensor(T, d, bits8):
     assert r["h"].data_ptr() == add.data_ptr() and torch.equal(x, kept)
     for name in ("h", "y", "rstd") + (("codes", "scales") if bits8 else ()):
         assert torch.equal(r[name], want[name]), name
+
+
+@pytest.mark.parametrize("E", [7, 64, 256])
+def test_probabilities_far_below_the_largest(E):
+    """A sequence for each token, so that probs is p.  In units of 2^-24 of p, with x = logit - largest: the difference |x|,
+    its product with log2 e |x| and a quarter for the constant, ex2 4; the sum of E exponentials 4 and a chain of 35; the
+    reciprocal and the product 2, the mean's one."""
+    g = torch.Generator(DEV).manual_seed(E)
+    T = 3000
+    logits = torch.randn((T, E), generator=g, device=DEV) - 86 * torch.rand((T, E), generator=g, device=DEV)
+    logits += 1000 * torch.rand((T, 1), generator=g, device=DEV)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    probs = mk.mk_moe_balance_loss(logits, ids, torch.arange(T + 1, dtype=torch.int32, device=DEV))[2].to(F64)
+    l = logits.to(F64)
+    p, x = torch.softmax(l, 1), l.amax(1, keepdim=True) - l
+    assert float(x.max()) > 80
+    assert bool(((probs - p).abs() <= (2.25 * x + 46) * 2.0 ** -24 * p + 2.0 ** -126).all())
