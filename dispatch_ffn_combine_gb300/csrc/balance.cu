@@ -25,10 +25,10 @@
 // rows in block order.  Counts are integers.  The number of blocks depends on the
 // sizes alone: results repeat bit for bit.
 //
-// 32768 tokens of 256 experts in 23 sequences: the losses 21.6 us (two launches; 34 MB,
-// 5 us at the copy rate), the gradient 20 us (72 MB, 11 us).  Few warps are resident, with
+// 32768 tokens of 256 experts in 23 sequences: the losses 18.6 us (two launches; 34 MB,
+// 5 us at the copy rate), the gradient 16.2 us (72 MB, 11 us).  Few warps are resident, with
 // 32 logits and 32 sums or factors per lane, and each waits for its rows' loads: with 32
-// lanes per token 26 and 40 us, with a branch around each load 34 and 39.
+// lanes per token, in earlier forms, 26 and 40 us, with a branch around each load 34 and 39.
 #include <algorithm>
 
 #include "mk_device.cuh"
@@ -150,9 +150,9 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// e^x for x <= 0 as 2^(x log2 e), below 2^-126 zero: off by the rounding of the product
-// (2^-24 |x| log2 e) and 2^-22, both relative, so 1e-6 at most where e^x is above 1e-3,
-// and a fourth of expf's instructions, which took half of the kernels' issue slots.
+// e^x for x <= 0 as 2^(x log2 e), below 2^-126 zero: off by (1.25 |x| + 4) 2^-24 of itself, the
+// product's rounding and log2 e's, and ex2's 2^-22.  x, the difference of two fp32 logits, is off by |x| 2^-24
+// already, which expf does not mend; with it the losses take 20.4 us for 18.6, the gradient 17.7 for 16.2.
 __device__ __forceinline__ float exp_down(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));

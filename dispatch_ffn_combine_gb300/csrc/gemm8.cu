@@ -32,8 +32,8 @@
 //               reads and multiplies four blocks' at a time.  With the producer issuing
 //               them in slots of four, and two reads per block, they came late and cost
 //               100 cycles of a block's 1030 (131072 skewed rows of 4096 to 1536 columns:
-//               731 us, from then on 700, with slots of sixteen 679).  Without any scales it would
-//               be 619; loads from global memory in the epilogue warps held up their other waits.
+//               731 us, in that form without any scales 619; from then on 700, with slots of sixteen
+//               679).  Loads from global memory in the epilogue warps held up their other waits.
 //   roles       the producer, the issuer and the scales' thread are single threads: per block of
 //               columns their waits and issues are one after the other, and with
 //               a whole warp voting on each wait they took longer than the MMAs.
@@ -45,10 +45,12 @@
 //               What bounds the kernel with many rows is the epilogue warps' own
 //               time per block, one step after the other: a wait takes 150 to 200 cycles
 //               though the phase is long complete, so the next one is tested while the last
-//               additions run (653 us, so 620; it was no gain with N = 256); reads and additions
-//               350, what is around them 150, scales 30, with 512 of MMAs beside them.
+//               additions run (653 us, so 620; it was no gain with N = 256).  Reads and additions
+//               take 350, what is around them 150, scales 30, with 512 of MMAs beside them (clocks
+//               read in a copy of the form with N = 256).
 //               Uniform waits, predicated arrives and additions in pairs: 700 us to 662.
-//               65536 rows over 16 experts, 7168 to 4096, reach 3130 TFLOP/s.
+//               Waits with acquire at cluster scope, since the peer's copies and commits complete
+//               the barriers: 629 us to 637.
 //               Sixteen epilogue warps of 64 columns, reads ahead of the additions, scales a block
 //               ahead, and one lane waiting for its warp were slower.
 //   store       32 rows of 128 bytes at a time through swizzled shared memory to
@@ -56,6 +58,10 @@
 //               next expert's rows share, in plain stores from there.
 //   schedule    tile-slot and stage rings, relays and bounded waits as in the
 //               weight-gradient kernel.
+//
+// Times above are of captured calls, four in a row after a rest, with codes of normal values.  Called for
+// seconds, at the power cap, the skewed case takes 732 us.  65536 rows over 16 equal experts, 7168 to 4096:
+// 2970 TFLOP/s after a rest, 2620 for seconds (codes drawn evenly from 0 to 119: 3070 and 2760).
 #include <algorithm>
 #include <atomic>
 
@@ -335,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tmOut);
     }
     // The stages' rows start as zero.  Rows that no copy has written are multiplied all the same, and zeros take
-    // less power than what lay there (1024 rows over 256 experts, 7168 to 2048: 636 us, so 603; for seconds at the
-    // power cap 730, so 660).
+    // less power than what lay there (1024 rows over 256 experts, 7168 to 2048: 636 us after a rest, so 603; for
+    // seconds at the power cap 730, so 660).
     for (uint32_t i = threadIdx.x; i < kStages * (kHalfBytes / 16); i += kThreads)
         st_shared_v4(smem_u32(smem + i / (kHalfBytes / 16) * kStageBytes + i % (kHalfBytes / 16) * 16), make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_shared();

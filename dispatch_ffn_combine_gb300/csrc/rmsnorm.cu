@@ -16,9 +16,9 @@
 // next rows into shared memory while the current row is reduced, and the row's sum
 // is the only point where its warps meet.  A block of 128 values lies in 16
 // neighbouring lanes' vectors, so its scale takes four shuffles and no barrier.
-// 32768 x 7168 bf16: forward with an addition 304 us (0.91 of the copy rate), with codes
-// as well 358 to 372 (0.84 to 0.87; 28 warps with half the values each 373 to 381), backward
-// with a residual 280 (0.98).
+// 32768 x 7168 bf16: forward with an addition 302 us (0.91 of the copy rate), with codes
+// as well 355 to 368 (0.85 to 0.88; 28 warps with half the values each were up to 5 % slower), with codes
+// alone 264 (0.92), backward with a residual 277 (0.98).
 #include <algorithm>
 
 #include "norm_rows.cuh"

@@ -67,7 +67,8 @@ def forward(block: MoEBlock, x: torch.Tensor, seq_offsets: torch.Tensor | None =
 
     seq_offsets [B + 1] int32 bounds the sequences of the router's losses (None: one of all tokens; tokens behind
     the last one have no part in them); with a coefficient that is not 0, what is saved holds them: "losses"
-    [balance, z] fp32.  Their logits are fp32, the gate's product left to torch.
+    [balance, z] fp32.  Their logits are the gate's product in fp32, left to torch (with its switch for tf32 on, which
+    is off by default, they are rounded more than those that the router chose by).
 
     The layer works on bf16 whatever x is: the norm's output, gate, up, h, each expert's output and their
     sum y are rounded to it, as in the forward layer; the residual sum is in x's type."""

@@ -553,7 +553,9 @@ MK_API mk_status mk_moe_rmsnorm_bwd(const void* dy, const void* h, int x_type, c
  *        tokens (B = 1).  Tokens behind the last sequence have no part.
  *   loss fp32 [2], counts int32 [B, E], probs fp32 [B, E] (out)
  *   ws: at least mk_moe_balance_workspace_size(T, E, k, B) bytes.
- * A token whose logits are all -inf has p = 0 and no part in z.  Ids outside
+ * A token whose logits are all -inf has p = 0 and no part in z.  p is worked out in fp32:
+ * within (2.25 x + 46) 2^-24 of itself for a logit x below the token's largest, and zero
+ * below 2^-126; no fp32 sum over tokens is a chain of more than 2048.  Ids outside
  * [0, E) (not counted) or bad offsets set MK_ERR_BOUNDS on the device and the
  * losses are NaN.  Limits: E <= 256, k <= min(E, 8), B <= 65535, T * k < 2^31. */
 MK_API size_t mk_moe_balance_workspace_size(int64_t T, int E, int k, int B);
