@@ -370,7 +370,7 @@ inline int grid_blocks(const RowShape& s, int64_t rows, int d, int most) {
 }
 
 // Rows that a row group of a backward pass adds up in one fp32 sum per column.  A chain of n additions is off by up to n
-// 2^-24 of its terms' magnitudes, so more rows than that per group (a million for long rows, ten for short ones) go through the
+// 2^-24 of its terms' magnitudes, so more rows than that per group (0.6 million for long rows, 20 for short ones) go through the
 // kernel in pieces, whose sums are added: 2^-12 for a piece and 2^-24 for each.  The rows of a piece are a multiple of 8, so that it
 // starts on a 16-byte word as the tensor does.
 constexpr int kMaxChain = 4096;
